@@ -11,8 +11,12 @@
  *
  * and, around them: the folded projections (mla_fold_weights,
  * mla_absorb_q_folded, mla_up_o_folded), the YaRN-scaled RoPE table and score
- * scale, and a low-bit cache format with its own append and decode
- * (mla_rope_append_e4m3, mla_decode_e4m3).
+ * scale, a low-bit cache format with its own append and decode
+ * (mla_rope_append_e4m3, mla_decode_e4m3), and the layer around the decode:
+ * norms and residual (mla_block_norm), projections in 8-bit integers
+ * (mla_quantize_i8, mla_linear_i8), the append from the projections' rows
+ * (mla_norm_rope_append) and the decode of a batch behind one shared prefix
+ * (mla_decode_shared).
  *
  * Sources (page title, section / equation):
  *   [notes]  "MLA(Multi-head Latent Attention): DeepSeek-V2 논문정리":
@@ -365,6 +369,124 @@ int mla_decode_e4m3(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf
                     int max_blocks_per_seq, const int32_t* seq_lens, int B, int T_q,
                     int max_splits, void* workspace, size_t ws_bytes,
                     mla_bf16* out_latent, float* out_lse, void* stream);
+
+/* ---- The layer around the decode -----------------------------------------
+ * The steps of an attention layer that surround the absorbed decode when a
+ * batch is served ([notes] "MLA 코드 구현" forward gives their order; the
+ * DeepSeek-V2 layer norms both compressed latents before use): a norm in
+ * front of the layer, the projections, the append, the decode of a batch
+ * behind one prompt, the output projection and the residual add. */
+
+/* mla_decode for a batch whose sequences begin with the same cache pages (a
+ * system prompt, few-shot examples): the same scores, mask, softmax, outputs
+ * and size limits, with the keys of the shared pages read once for all query
+ * rows of the batch instead of once per sequence.
+ *   shared_table (n_shared) int32: the blocks of the shared pages, which hold
+ *     the first 64 * n_shared keys of every sequence.  Only whole pages are
+ *     shared.  n_shared = 0 shares nothing (shared_table may be NULL).
+ *   block_table  (B, max_blocks_per_seq) int32 as for mla_decode, indexed by
+ *     the key's position in the whole sequence; entries [0, n_shared) are not
+ *     read.  n_shared <= max_blocks_per_seq <= 2^24.
+ *   seq_lens     (B) int32, the whole length after the step's append, shared
+ *     keys included; every query token must lie behind the shared pages:
+ *     64 * n_shared + T_q <= seq_lens[b] <= 64 * max_blocks_per_seq.  A
+ *     sequence that breaks this sets MLA_STATUS_BAD_SEQ_LEN; its outputs are
+ *     zero and -inf.
+ * The shared and the own keys of a row are scored in separate units of work
+ * and always merged by the log-sum-exp reduction.  tcgen05 kernels (cfg->impl
+ * 0 or 2): d_c = 512, d_r = 64 and any n_h -- the query rows of the batch are
+ * taken 128 at a time against the shared keys, whatever their heads.  Portable
+ * kernels: every supported shape.  max_splits as for mla_decode, for each of
+ * the two key ranges. */
+int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf16* q_r,
+                      const mla_bf16* pool, int num_blocks, const int32_t* shared_table, int n_shared,
+                      const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                      int B, int T_q, int max_splits, void* workspace, size_t ws_bytes,
+                      mla_bf16* out_latent, float* out_lse, void* stream);
+
+/* Workspace bytes of mla_decode_shared (256-byte aligned pointer; starts with
+ * the device status word); 0 for invalid arguments. */
+size_t mla_decode_shared_workspace_bytes(const mla_config_t* cfg, int B, int T_q, int max_splits);
+
+/* Rows of a bf16 matrix as 8-bit integers with one float32 scale each:
+ *   scale[n] = max_k |x[n, k]| / 127,  x8[n, k] = round(127 x[n, k] / max)
+ * (float32, round to nearest even; both quotients correctly rounded, so the
+ * codes are those of exact arithmetic).  A row of zeros has scale 0 and zero
+ * codes.  Inputs must be finite.  For activations (a scale per token) and,
+ * once per weight set, for weights (a scale per output channel).
+ *   x     (n_rows, d) bf16, rows ld_x elements apart (ld_x >= d, multiples of 8)
+ *   x8    (n_rows, d) int8, dense, 16-byte aligned;  scale (n_rows) float32
+ * 1 <= n_rows <= 2^24, 16 <= d <= 65536, d a multiple of 16. */
+int mla_quantize_i8(const mla_bf16* x, int64_t ld_x, int n_rows, int d, int8_t* x8, float* scale,
+                    void* stream);
+
+/* Projection in 8-bit integers:
+ *   out[n, o] = (sum_k x8[n, k] w8[o, k]) x_scale[n] w_scale[o]
+ * (the sum exact in 32-bit integers, the two float32 products and one
+ * rounding to bf16).  w8 in any of the layer's dense weights' own layout:
+ * W^DQ and W^DKV (one above the other), W^UQ, W^O, or the folded F and G.
+ *   x8 (n_tok, d_in) int8, rows ld_x bytes apart (ld_x >= d_in, a multiple of
+ *   16);  w8 (d_out, d_in) int8;  x_scale (n_tok), w_scale (d_out) float32
+ *   out (n_tok, d_out) bf16;  dev_status as for mla_absorb_q
+ * 1 <= n_tok <= 65536, 16 <= d_in <= 65536 and a multiple of 16, 8 <= d_out <=
+ * 131072 and a multiple of 8.  x8, w8 and out are 16-byte aligned. */
+int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const int8_t* w8,
+                  const float* w_scale, mla_bf16* out, int n_tok, int d_in, int d_out,
+                  int32_t* dev_status, void* stream);
+
+/* The end of one block and the norm in front of the next, in one pass over
+ * each token's row (float32 throughout, each output rounded once):
+ *   x = u                                            (the block's output)
+ *   x = x / sqrt(mean(x^2) + eps) * w_post           if w_post
+ *   x = gate * x                                     if gate
+ *   r = residual + alpha * x                         if residual, else r = x
+ *   y = r / sqrt(mean(r^2) + eps) * w_pre            if w_pre
+ * y is taken from r before r is rounded.  Without w_post, gate and residual
+ * this is an RMSNorm (of c^Q, or in front of the first block).
+ *   u (n_tok, d) bf16, rows ld_u elements apart;  w_post, w_pre (d) bf16
+ *   gate: rows ld_gate elements apart, or one row for all tokens (ld_gate = 0)
+ *   residual (n_tok, d) bf16;  residual_out (n_tok, d) bf16 receives r; it may
+ *     be NULL, residual itself, or (with residual NULL) must be NULL
+ *   out  (n_tok, d) bf16 receives y;  out8 (n_tok, d) int8 and out8_scale
+ *     (n_tok) receive y quantised by the rule of mla_quantize_i8 from its
+ *     float32 value.  Any of the three outputs may be NULL, not all; out and
+ *     out8 need w_pre, and w_pre needs one of them.
+ * d a multiple of 8, 8 <= d <= 16384 (out8: a multiple of 16); ld_u >= d, ld_gate
+ * 0 or >= d, both multiples of 8; bf16 and int8 pointers 16-byte aligned; eps > 0;
+ * alpha finite.  1 <= n_tok <= 2^24.  Outputs may not overlap inputs, other
+ * than residual_out = residual. */
+int mla_block_norm(const mla_bf16* u, int64_t ld_u, const mla_bf16* w_post, const mla_bf16* gate,
+                   int64_t ld_gate, float alpha, const mla_bf16* residual, mla_bf16* residual_out,
+                   const mla_bf16* w_pre, float eps, int n_tok, int d, mla_bf16* out, int8_t* out8,
+                   float* out8_scale, void* stream);
+
+/* mla_rope_append from the projections' own rows: the latent is normed and
+ * the query split on the way.  For token n = b * T_q + t with p = positions[n]:
+ *   c = kv[n, 0:d_c];  c = c / sqrt(mean(c^2) + eps) * w_kv, rounded to bf16
+ *   cache row of p <- c || RoPE(kv[n, d_c:d_c+d_r], p)     (as mla_rope_append)
+ *   q_c[n, i, :] <- q[n, i, 0:d_h]                          (bit copy)
+ *   q_r[n, i, :] <- RoPE(q[n, i, d_h:d_h+d_r], p)
+ *   q  (n_tok, n_h, d_h + d_r) bf16, the rows of the query up-projection; q,
+ *      q_c and q_r may be NULL together (a cache fill without queries)
+ *   kv (n_tok, d_c + d_r) bf16, rows ld_kv elements apart (ld_kv >= d_c + d_r,
+ *      a multiple of 8): W^DKV's rows, or the last columns of a wider product
+ *   w_kv (d_c) bf16;  eps > 0;  rope_table 16-byte aligned;
+ *      the rest as for mla_rope_append
+ *   q_c (n_tok, n_h, d_h), q_r (n_tok, n_h, d_r) bf16, dense, apart from q
+ * A token whose position is invalid sets MLA_STATUS_BAD_POSITION and leaves
+ * q_c, q_r and the cache as they were; one whose block is invalid sets
+ * MLA_STATUS_BAD_BLOCK and leaves the cache.  The _e4m3 form appends to the
+ * low-bit cache: the normed bf16 latent quantised as in mla_rope_append_e4m3. */
+int mla_norm_rope_append(const mla_config_t* cfg, const mla_bf16* q, const mla_bf16* kv, int64_t ld_kv,
+                         const mla_bf16* w_kv, float eps, const int32_t* positions,
+                         const float* rope_table, int max_pos, const int32_t* block_table,
+                         int max_blocks_per_seq, mla_bf16* pool, int num_blocks, int B, int T_q,
+                         mla_bf16* q_c, mla_bf16* q_r, int32_t* dev_status, void* stream);
+int mla_norm_rope_append_e4m3(const mla_config_t* cfg, const mla_bf16* q, const mla_bf16* kv,
+                              int64_t ld_kv, const mla_bf16* w_kv, float eps, const int32_t* positions,
+                              const float* rope_table, int max_pos, const int32_t* block_table,
+                              int max_blocks_per_seq, uint8_t* pool, int num_blocks, int B, int T_q,
+                              mla_bf16* q_c, mla_bf16* q_r, int32_t* dev_status, void* stream);
 
 /* Zero a device status word (async on stream). */
 int mla_clear_status(int32_t* dev_status, void* stream);

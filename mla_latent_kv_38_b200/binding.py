@@ -31,6 +31,8 @@ EXPORTED = (
     "mla_decode_noalloc", "mla_decode_split_counts", "mla_test_arm_decode_timeout", "mla_up_v",
     "mla_fold_weights", "mla_absorb_q_folded", "mla_up_o_folded_workspace_bytes", "mla_up_o_folded",
     "mla_e4m3_row_bytes", "mla_rope_append_e4m3", "mla_decode_e4m3_workspace_bytes", "mla_decode_e4m3",
+    "mla_decode_shared_workspace_bytes", "mla_decode_shared", "mla_quantize_i8", "mla_linear_i8",
+    "mla_block_norm", "mla_norm_rope_append", "mla_norm_rope_append_e4m3",
     "mla_clear_status", "mla_read_status",
 )
 
@@ -97,6 +99,17 @@ _lib.mla_rope_append_e4m3.argtypes = [_cfgp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _
 _lib.mla_decode_e4m3_workspace_bytes.restype = _sz
 _lib.mla_decode_e4m3_workspace_bytes.argtypes = [_cfgp, _i, _i, _i]
 _lib.mla_decode_e4m3.argtypes = [_cfgp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _sz, _vp, _vp, _vp]
+_i64, _f = ctypes.c_int64, ctypes.c_float
+_lib.mla_decode_shared_workspace_bytes.restype = _sz
+_lib.mla_decode_shared_workspace_bytes.argtypes = [_cfgp, _i, _i, _i]
+_lib.mla_decode_shared.argtypes = [_cfgp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _sz, _vp, _vp,
+                                   _vp]
+_lib.mla_quantize_i8.argtypes = [_vp, _i64, _i, _i, _vp, _vp, _vp]
+_lib.mla_linear_i8.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
+_lib.mla_block_norm.argtypes = [_vp, _i64, _vp, _vp, _i64, _f, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _vp, _vp]
+_lib.mla_norm_rope_append.argtypes = [_cfgp, _vp, _vp, _i64, _vp, _f, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp,
+                                      _vp, _vp]
+_lib.mla_norm_rope_append_e4m3.argtypes = _lib.mla_norm_rope_append.argtypes
 _lib.mla_clear_status.argtypes = [_vp, _vp]
 _lib.mla_read_status.argtypes = [_vp, _vp, _vp]
 
@@ -269,6 +282,65 @@ def mla_decode_e4m3(cfg: MlaConfig, q_abs, q_r, pool, num_blocks: int, block_tab
         ctypes.byref(cfg), _ptr(q_abs), _ptr(q_r), _ptr(pool), int(num_blocks), _ptr(block_table),
         int(max_blocks_per_seq), _ptr(seq_lens), int(B), int(T_q), int(max_splits), _ptr(workspace),
         int(ws_bytes), _ptr(out_latent), _ptr(out_lse), _stream(stream)))
+
+
+def mla_decode_shared_workspace_bytes(cfg: MlaConfig, B: int, T_q: int, max_splits: int = 0) -> int:
+    return int(_lib.mla_decode_shared_workspace_bytes(ctypes.byref(cfg), int(B), int(T_q), int(max_splits)))
+
+
+def mla_decode_shared(cfg: MlaConfig, q_abs, q_r, pool, num_blocks: int, shared_table, n_shared: int, block_table,
+                      max_blocks_per_seq: int, seq_lens, B: int, T_q: int, max_splits: int,
+                      workspace, ws_bytes: int, out_latent, out_lse, stream=None):
+    """mla_decode of a batch whose sequences share their first n_shared cache pages."""
+    _check("mla_decode_shared", _lib.mla_decode_shared(
+        ctypes.byref(cfg), _ptr(q_abs), _ptr(q_r), _ptr(pool), int(num_blocks), _ptr(shared_table), int(n_shared),
+        _ptr(block_table), int(max_blocks_per_seq), _ptr(seq_lens), int(B), int(T_q), int(max_splits), _ptr(workspace),
+        int(ws_bytes), _ptr(out_latent), _ptr(out_lse), _stream(stream)))
+
+
+def mla_quantize_i8(x, ld_x: int, n_rows: int, d: int, x8, scale, stream=None):
+    """Rows of a bf16 matrix (ld_x elements apart) as int8 codes with a float32 scale each."""
+    _check("mla_quantize_i8", _lib.mla_quantize_i8(_ptr(x), int(ld_x), int(n_rows), int(d), _ptr(x8), _ptr(scale),
+                                                   _stream(stream)))
+
+
+def mla_linear_i8(x8, ld_x: int, x_scale, w8, w_scale, out, n_tok: int, d_in: int, d_out: int, dev_status=None,
+                  stream=None):
+    """out = (x8 w8^T) x_scale w_scale in bf16: an int8 projection with scales per token and output channel."""
+    _check("mla_linear_i8", _lib.mla_linear_i8(_ptr(x8), int(ld_x), _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(out),
+                                               int(n_tok), int(d_in), int(d_out), _ptr(dev_status), _stream(stream)))
+
+
+def mla_block_norm(u, ld_u: int, w_post, gate, ld_gate: int, alpha: float, residual, residual_out, w_pre, eps: float,
+                   n_tok: int, d: int, out=None, out8=None, out8_scale=None, stream=None):
+    """Block output normed, gated, scaled and added to the residual, and the next block's norm (bf16 and / or int8)."""
+    _check("mla_block_norm", _lib.mla_block_norm(
+        _ptr(u), int(ld_u), _ptr(w_post), _ptr(gate), int(ld_gate), float(alpha), _ptr(residual), _ptr(residual_out),
+        _ptr(w_pre), float(eps), int(n_tok), int(d), _ptr(out), _ptr(out8), _ptr(out8_scale), _stream(stream)))
+
+
+def _norm_rope_append(name, cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
+                      max_blocks_per_seq, pool, num_blocks, B, T_q, q_c, q_r, dev_status, stream):
+    _check(name, getattr(_lib, name)(
+        ctypes.byref(cfg), _ptr(q), _ptr(kv), int(ld_kv), _ptr(w_kv), float(eps), _ptr(positions), _ptr(rope_table),
+        int(max_pos), _ptr(block_table), int(max_blocks_per_seq), _ptr(pool), int(num_blocks), int(B), int(T_q),
+        _ptr(q_c), _ptr(q_r), _ptr(dev_status), _stream(stream)))
+
+
+def mla_norm_rope_append(cfg: MlaConfig, q, kv, ld_kv: int, w_kv, eps: float, positions, rope_table, max_pos: int,
+                         block_table, max_blocks_per_seq: int, pool, num_blocks: int, B: int, T_q: int, q_c=None,
+                         q_r=None, dev_status=None, stream=None):
+    """mla_rope_append from the projections' rows: latent normed, query split into q_c and rotated q_r."""
+    _norm_rope_append("mla_norm_rope_append", cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
+                      max_blocks_per_seq, pool, num_blocks, B, T_q, q_c, q_r, dev_status, stream)
+
+
+def mla_norm_rope_append_e4m3(cfg: MlaConfig, q, kv, ld_kv: int, w_kv, eps: float, positions, rope_table, max_pos: int,
+                              block_table, max_blocks_per_seq: int, pool, num_blocks: int, B: int, T_q: int, q_c=None,
+                              q_r=None, dev_status=None, stream=None):
+    """mla_norm_rope_append into an e4m3 pool."""
+    _norm_rope_append("mla_norm_rope_append_e4m3", cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos,
+                      block_table, max_blocks_per_seq, pool, num_blocks, B, T_q, q_c, q_r, dev_status, stream)
 
 
 def mla_clear_status(dev_status, stream=None):

@@ -145,6 +145,7 @@ struct DecodeParams {
     const uint16_t* pool;       // (num_blocks, block_size, d_c + d_r)
     const uint8_t* pool8 = nullptr;   // e4m3 pool (portable kernel only), else null
     const int32_t* block_table; // (B, max_blocks)
+    const int32_t* shared_table = nullptr;   // (n_shared) blocks of the pages every sequence begins with
     const int32_t* seq_lens;    // (B)
     uint16_t* out_latent;       // (n_tok, n_h, d_c)
     float* out_lse;             // (n_tok, n_h)
@@ -152,6 +153,7 @@ struct DecodeParams {
     float* part_lse;            // (splits, n_tok, n_h)
     int32_t* status;
     int n_h, d_c, d_r, block_size;
+    int n_shared = 0;           // shared pages (the shared decode only)
     int num_blocks, max_blocks, B, T_q, n_tok, splits;
     float scale_log2;           // scale * log2(e)
 };

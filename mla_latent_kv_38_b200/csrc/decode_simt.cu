@@ -45,7 +45,12 @@ __device__ __forceinline__ void load8(const unsigned char* tile, int row_stride,
 // plus 16 bytes (the padding spreads the rows over the shared-memory banks).
 __host__ __device__ __forceinline__ int staged_row_bytes(int D, bool e4m3) { return (e4m3 ? 4 : 2) * D + 16; }
 
-template <bool kE4m3>
+// kShared: the decode of a batch that shares its first P.n_shared pages.  Grid
+// (groups, split): the first groups take 32 consecutive query rows of the whole
+// batch (whatever their token and head) against the shared pages, the others
+// a token's 32 heads against its sequence's own pages; every row ends up with
+// `splits` partials of each kind, which the merge joins.
+template <bool kE4m3, bool kShared>
 __global__ void __launch_bounds__(256, 2)
 decode_simt_kernel(DecodeParams P) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -54,17 +59,39 @@ decode_simt_kernel(DecodeParams P) {
     unsigned char* tile = smem_raw;                                          // [32][row_bytes]
     uint16_t* Qs = reinterpret_cast<uint16_t*>(smem_raw + kSimtKeys * row_bytes);  // [heads][D] bf16
 
-    const int split = blockIdx.x, n = blockIdx.y, hg = blockIdx.z;
-    const int b = n / P.T_q, t = n - b * P.T_q;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head0 = hg * kSimtHeads + warp * kHeadsPerWarp;   // this warp's heads: head0, head0 + 1
-    const bool warp_ok = head0 < P.n_h;
+    int split, n, hg;
+    bool prefix = false;   // kShared: this block scores the shared pages
+    if constexpr (kShared) {
+        const int row_groups = static_cast<int>((static_cast<long>(P.n_tok) * P.n_h + kSimtHeads - 1) / kSimtHeads);
+        const int hgs = (P.n_h + kSimtHeads - 1) / kSimtHeads;
+        const int g = static_cast<int>(blockIdx.x) - row_groups;
+        split = blockIdx.y;
+        prefix = g < 0;
+        n = prefix ? 0 : g / hgs;
+        hg = prefix ? static_cast<int>(blockIdx.x) : g - n * hgs;
+    } else {
+        split = blockIdx.x, n = blockIdx.y, hg = blockIdx.z;
+    }
+    const int b = n / P.T_q, t = n - b * P.T_q;
+    // the block's query rows: consecutive from first_row on, rows_here of them
+    // (a token's heads, or with `prefix` any of the batch's rows)
+    const size_t row_base = static_cast<size_t>(n) * P.n_h;
+    const long row_count = kShared && prefix ? static_cast<long>(P.n_tok) * P.n_h : P.n_h;
+    const long head0 = static_cast<long>(hg) * kSimtHeads + warp * kHeadsPerWarp;   // this warp's rows: head0 ..
+    const bool warp_ok = head0 < row_count;
 
     int L = P.seq_lens[b];
-    const bool len_ok = L >= P.T_q && L <= P.max_blocks * P.block_size;
-    if (!len_ok && threadIdx.x == 0 && split == 0 && hg == 0 && t == 0)
+    const int own0 = kShared ? P.n_shared * P.block_size : 0;   // keys in front of the sequence's own
+    const bool len_ok = L >= P.T_q + own0 && L <= P.max_blocks * P.block_size;
+    if (!len_ok && !prefix && threadIdx.x == 0 && split == 0 && hg == 0 && t == 0)
         raise_status(P.status, MLA_STATUS_BAD_SEQ_LEN);
-    const int kv_len = len_ok ? L - P.T_q + t + 1 : 0;
+    const int32_t* table = P.block_table + static_cast<size_t>(b) * P.max_blocks + (kShared ? P.n_shared : 0);
+    int kv_len = len_ok ? L - P.T_q + t + 1 - own0 : 0;
+    if (kShared && prefix) {
+        table = P.shared_table;
+        kv_len = own0;
+    }
     const int ntiles = (kv_len + kSimtKeys - 1) / kSimtKeys;
     const int per = (ntiles + P.splits - 1) / P.splits;
     const int tile0 = split * per;
@@ -73,11 +100,10 @@ decode_simt_kernel(DecodeParams P) {
     // stage the query rows as bf16 (the score scale is applied to each dot product)
     for (int e = threadIdx.x; e < kSimtHeads * D; e += blockDim.x) {
         const int w = e / D, c = e - w * D;
-        const int hh = hg * kSimtHeads + w;
+        const long hh = static_cast<long>(hg) * kSimtHeads + w;
         uint16_t v = 0;
-        if (hh < P.n_h) {
-            v = c < P.d_c ? P.q_abs[(static_cast<size_t>(n) * P.n_h + hh) * P.d_c + c]
-                          : P.q_r[(static_cast<size_t>(n) * P.n_h + hh) * P.d_r + (c - P.d_c)];
+        if (hh < row_count) {
+            v = c < P.d_c ? P.q_abs[(row_base + hh) * P.d_c + c] : P.q_r[(row_base + hh) * P.d_r + (c - P.d_c)];
         }
         Qs[e] = v;
     }
@@ -108,7 +134,7 @@ decode_simt_kernel(DecodeParams P) {
                 const int key = kt * kSimtKeys + j;
                 const unsigned char* src = nullptr;
                 if (key < kv_len) {
-                    const int blk = P.block_table[static_cast<size_t>(b) * P.max_blocks + key / P.block_size];
+                    const int blk = table[key / P.block_size];
                     if (blk >= 0 && blk < P.num_blocks)
                         src = P.pool8 + (static_cast<size_t>(blk) * P.block_size + key % P.block_size) * L.bytes;
                     else if (v == 0)
@@ -156,7 +182,7 @@ decode_simt_kernel(DecodeParams P) {
                 const int key = kt * kSimtKeys + j;
                 uint4 val = make_uint4(0, 0, 0, 0);
                 if (key < kv_len) {
-                    const int blk = P.block_table[static_cast<size_t>(b) * P.max_blocks + key / P.block_size];
+                    const int blk = table[key / P.block_size];
                     if (blk >= 0 && blk < P.num_blocks) {
                         const uint4* src = reinterpret_cast<const uint4*>(
                             P.pool + (static_cast<size_t>(blk) * P.block_size + key % P.block_size) * D);
@@ -231,13 +257,17 @@ decode_simt_kernel(DecodeParams P) {
 
 #pragma unroll
     for (int h = 0; h < kHeadsPerWarp; ++h) {
-        const int head = head0 + h;
-        if (head >= P.n_h) break;
-        const size_t row = static_cast<size_t>(n) * P.n_h + head;
-        const bool empty = l_run[h] == 0.f;
+        const long head = head0 + h;
+        if (head >= row_count) break;
+        const size_t row = row_base + head;
+        bool empty = l_run[h] == 0.f;
+        if (kShared && prefix) {   // rows of an invalid sequence see nothing
+            const int rl = P.seq_lens[row / P.n_h / P.T_q];
+            empty = empty || rl < P.T_q + own0 || rl > P.max_blocks * P.block_size;
+        }
         const float inv_l = empty ? 0.f : 1.f / l_run[h];
         const float lse = empty ? -INFINITY : (m_run[h] + __log2f(l_run[h])) * kLn2;
-        if (P.splits == 1) {
+        if (!kShared && P.splits == 1) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ch = lane + 32 * u;
@@ -252,7 +282,8 @@ decode_simt_kernel(DecodeParams P) {
             }
             if (lane == 0) P.out_lse[row] = lse;
         } else {
-            float* po = P.part_o + (static_cast<size_t>(split) * P.n_tok * P.n_h + row) * P.d_c;
+            const int part = kShared && !prefix ? P.splits + split : split;
+            float* po = P.part_o + (static_cast<size_t>(part) * P.n_tok * P.n_h + row) * P.d_c;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ch = lane + 32 * u;
@@ -264,7 +295,7 @@ decode_simt_kernel(DecodeParams P) {
                                        o[h][u][7] * inv_l);
                 }
             }
-            if (lane == 0) P.part_lse[static_cast<size_t>(split) * P.n_tok * P.n_h + row] = lse;
+            if (lane == 0) P.part_lse[static_cast<size_t>(part) * P.n_tok * P.n_h + row] = lse;
         }
     }
 }
@@ -311,7 +342,7 @@ size_t simt_smem_bytes(int d_c, int d_r, bool e4m3) {
 cudaError_t launch_decode_simt(const DecodeParams& P, cudaStream_t stream) {
     const bool e4m3 = P.pool8 != nullptr;
     const size_t smem = simt_smem_bytes(P.d_c, P.d_r, e4m3);
-    auto kernel = e4m3 ? decode_simt_kernel<true> : decode_simt_kernel<false>;
+    auto kernel = e4m3 ? decode_simt_kernel<true, false> : decode_simt_kernel<false, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     dim3 grid(P.splits, P.n_tok, (P.n_h + kSimtHeads - 1) / kSimtHeads);
@@ -320,6 +351,20 @@ cudaError_t launch_decode_simt(const DecodeParams& P, cudaStream_t stream) {
     if (e != cudaSuccess || P.splits == 1) return e;
     return launch_merge(P.part_o, P.part_lse, P.out_latent, P.out_lse, P.n_tok * P.n_h, P.d_c,
                         P.splits, stream);
+}
+
+cudaError_t launch_decode_shared_simt(const DecodeParams& P, cudaStream_t stream) {
+    const size_t smem = simt_smem_bytes(P.d_c, P.d_r, false);
+    cudaError_t e = cudaFuncSetAttribute(decode_simt_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const long rows = static_cast<long>(P.n_tok) * P.n_h;
+    const long groups = (rows + kSimtHeads - 1) / kSimtHeads + static_cast<long>(P.n_tok) * ((P.n_h + kSimtHeads - 1) / kSimtHeads);
+    decode_simt_kernel<false, true><<<dim3(static_cast<unsigned>(groups), P.splits), 256, smem, stream>>>(P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_merge(P.part_o, P.part_lse, P.out_latent, P.out_lse, static_cast<int>(rows), P.d_c, 2 * P.splits,
+                        stream);
 }
 
 cudaError_t launch_merge(const float* part_o, const float* part_lse, uint16_t* out_latent,

@@ -27,6 +27,7 @@ cudaError_t launch_rope_append(uint16_t* q_r, const uint16_t* k_r, const uint16_
 
 size_t simt_smem_bytes(int d_c, int d_r, bool e4m3);
 cudaError_t launch_decode_simt(const DecodeParams& P, cudaStream_t stream);
+cudaError_t launch_decode_shared_simt(const DecodeParams& P, cudaStream_t stream);
 cudaError_t launch_merge(const float* part_o, const float* part_lse, uint16_t* out_latent,
                          float* out_lse, int rows, int d_c, int splits, cudaStream_t stream);
 

@@ -1,0 +1,219 @@
+// Row kernels of the layer around the decode: the norms and residual between
+// two blocks, and the quantisation of rows to 8-bit integers.
+//
+// mla_block_norm, per token's row of d values (formulas in include/mla.h):
+//   x = rms(u) w_post, gated;  r = residual + alpha x;  y = rms(r) w_pre
+// Bound by memory: 2 d bytes for each of u, residual, r, y (and a per-token
+// gate) and two to four operations a value.  A row's values stay in registers
+// from the load to the last store, in float32; the sum of squares of r and the
+// largest |r w_pre| (the scale of an int8 output) go through one reduction, so
+// a row costs one block-wide exchange for each norm.
+
+#include "common.cuh"
+#include "kernels.h"
+#include "layer.h"
+
+namespace mla {
+namespace {
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// int8 code of v: round to nearest even, within +-127
+__device__ __forceinline__ uint32_t code_i8(float v) {
+    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(v)))) & 0xFFu;
+}
+
+__device__ __forceinline__ uint2 pack_codes(const float* v) {
+    uint2 r;
+    r.x = code_i8(v[0]) | (code_i8(v[1]) << 8) | (code_i8(v[2]) << 16) | (code_i8(v[3]) << 24);
+    r.y = code_i8(v[4]) | (code_i8(v[5]) << 8) | (code_i8(v[6]) << 16) | (code_i8(v[7]) << 24);
+    return r;
+}
+
+// Sum and maximum over the threads of one row: a warp (kWarpRow) or the block.
+// Consecutive block-wide calls alternate between two halves of `red`, so one
+// barrier each is enough: a half is written again only after a barrier that
+// every reader of its old values has passed.
+template <bool kWarpRow>
+__device__ __forceinline__ float2 row_reduce(float s, float m, float2 (*red)[32], int& turn) {
+    s = warp_sum(s);
+    m = warp_max(m);
+    if constexpr (kWarpRow) return make_float2(s, m);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float2* r = red[turn];
+    turn ^= 1;
+    if (lane == 0) r[warp] = make_float2(s, m);
+    __syncthreads();
+    const float2 v = lane < warps ? r[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(v.x), warp_max(v.y));
+}
+
+// V vectors of 8 values per thread; kWarpRow: a row per warp, else per block.
+template <int V, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) block_norm_kernel(const BlockNormArgs a) {
+    __shared__ float2 red[2][32];
+    griddep_launch_dependents();
+    griddep_wait();
+    int turn = 0;
+    const int nv = a.d >> 3;
+    const int T = kWarpRow ? 32 : blockDim.x;
+    const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+    const int per = kWarpRow ? blockDim.x >> 5 : 1;
+    const long row0 = static_cast<long>(blockIdx.x) * per + (kWarpRow ? threadIdx.x >> 5 : 0);
+    const float inv_d = 1.f / static_cast<float>(a.d);
+    for (long row = row0; row < a.n_tok; row += static_cast<long>(gridDim.x) * per) {
+        float x[V][8];
+        float s = 0.f, m = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int j = t + k * T;
+            if (j < nv) {
+                unpack8(reinterpret_cast<const uint4*>(a.u + row * a.ld_u)[j], x[k]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
+        }
+        float rstd = 1.f;
+        if (a.w_post != nullptr) rstd = rsqrtf(row_reduce<kWarpRow>(s, 0.f, red, turn).x * inv_d + a.eps);
+        s = 0.f;
+        float y[V][8];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int j = t + k * T;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[k][e] = 0.f;
+            if (j >= nv) continue;
+            float f[8];
+            if (a.w_post != nullptr) {
+                unpack8(reinterpret_cast<const uint4*>(a.w_post)[j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * rstd * f[e];
+            }
+            if (a.gate != nullptr) {
+                unpack8(reinterpret_cast<const uint4*>(a.gate + row * a.ld_gate)[j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] *= f[e];
+            }
+            if (a.residual != nullptr) {
+                unpack8(reinterpret_cast<const uint4*>(a.residual + row * a.d)[j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = fmaf(a.alpha, x[k][e], f[e]);
+            }
+            if (a.residual_out != nullptr)
+                reinterpret_cast<uint4*>(a.residual_out + row * a.d)[j] = pack8(x[k]);
+            if (a.w_pre != nullptr) {
+                unpack8(reinterpret_cast<const uint4*>(a.w_pre)[j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s = fmaf(x[k][e], x[k][e], s);
+                    y[k][e] = x[k][e] * f[e];
+                    m = fmaxf(m, fabsf(y[k][e]));
+                }
+            }
+        }
+        if (a.w_pre == nullptr) continue;
+        const float2 tot = row_reduce<kWarpRow>(s, m, red, turn);
+        rstd = rsqrtf(tot.x * inv_d + a.eps);
+        // the norm's factor is common to the row: the codes follow from r w_pre alone
+        const float inv = tot.y > 0.f ? __fdiv_rn(127.f, tot.y) : 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int j = t + k * T;
+            if (j >= nv) continue;
+            if (a.out8 != nullptr) {
+                float c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) c[e] = y[k][e] * inv;
+                reinterpret_cast<uint2*>(a.out8 + row * a.d)[j] = pack_codes(c);
+            }
+            if (a.out != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[k][e] *= rstd;
+                reinterpret_cast<uint4*>(a.out + row * a.d)[j] = pack8(y[k]);
+            }
+        }
+        if (a.out8 != nullptr && t == 0) a.out8_scale[row] = __fdiv_rn(tot.y * rstd, 127.f);
+    }
+}
+
+// Codes and scale of a bf16 row: scale = max / 127, code = round(127 x / max).
+// 127 x is exact in float32 (8 + 7 bits), and the quotient is correctly
+// rounded: it meets a half only where the exact one does, because a quotient
+// of two 8-bit mantissas times 254 that is no integer is at least 2^-17 of
+// itself away from one.  So the codes are those of exact arithmetic.
+constexpr int kQuantCached = 4;   // vectors of a row that a thread keeps (d up to 8 x 4 x 512 = 16,384)
+
+__global__ void __launch_bounds__(512) quantize_i8_kernel(const uint16_t* __restrict__ x, long ld_x, int n_rows, int d,
+                                                          int8_t* __restrict__ x8, float* __restrict__ scale) {
+    __shared__ float2 red[2][32];
+    griddep_launch_dependents();
+    griddep_wait();
+    int turn = 0;
+    const int nv = d >> 3, T = blockDim.x, t = threadIdx.x;
+    for (long row = blockIdx.x; row < n_rows; row += gridDim.x) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + row * ld_x);
+        uint4 v[kQuantCached];
+        float m = 0.f;
+        auto fold = [&](const uint4& w) {
+            float f[8];
+            unpack8(w, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+        };
+#pragma unroll
+        for (int k = 0; k < kQuantCached; ++k)
+            v[k] = t + k * T < nv ? src[t + k * T] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kQuantCached; ++k) fold(v[k]);
+        for (int j = t + kQuantCached * T; j < nv; j += T) fold(src[j]);
+        const float amax = row_reduce<false>(0.f, m, red, turn).y;
+        auto emit = [&](const uint4& w, int j) {
+            float f[8];
+            unpack8(w, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = amax > 0.f ? __fdiv_rn(127.f * f[e], amax) : 0.f;
+            reinterpret_cast<uint2*>(x8 + row * d)[j] = pack_codes(f);
+        };
+#pragma unroll
+        for (int k = 0; k < kQuantCached; ++k)
+            if (t + k * T < nv) emit(v[k], t + k * T);
+        for (int j = t + kQuantCached * T; j < nv; j += T) emit(src[j], j);
+        if (t == 0) scale[row] = __fdiv_rn(amax, 127.f);
+    }
+}
+
+template <int V, bool kWarpRow>
+cudaError_t launch_norm(const BlockNormArgs& a, int threads, cudaStream_t stream) {
+    const int per = kWarpRow ? threads / 32 : 1;
+    const long want = (static_cast<long>(a.n_tok) + per - 1) / per;
+    const long most = 148L * (2048 / threads) * 4;
+    return launch_pdl(block_norm_kernel<V, kWarpRow>, dim3(static_cast<unsigned>(want < most ? want : most)),
+                      dim3(threads), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
+    const int nv = a.d / 8;
+    if (nv <= 32) return launch_norm<1, true>(a, 256, stream);
+    if (nv <= 64) return launch_norm<2, true>(a, 256, stream);
+    if (nv <= 1024) return launch_norm<1, false>(a, (nv + 31) / 32 * 32, stream);
+    return launch_norm<2, false>(a, (nv + 63) / 64 * 32, stream);
+}
+
+cudaError_t launch_quantize_i8(const uint16_t* x, long ld_x, int n_rows, int d, int8_t* x8, float* scale,
+                               cudaStream_t stream) {
+    const int nv = d / 8;
+    const int threads = nv >= 512 ? 512 : (nv + 31) / 32 * 32;
+    const int most = 148 * 16;
+    return launch_pdl(quantize_i8_kernel, dim3(n_rows < most ? n_rows : most), dim3(threads), 0, stream, x, ld_x,
+                      n_rows, d, x8, scale);
+}
+
+}  // namespace mla

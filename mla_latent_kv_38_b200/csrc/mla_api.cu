@@ -11,6 +11,7 @@
 #include "sm100_decode.h"
 #include "sm100_proj.h"
 #include "fold.h"
+#include "layer.h"
 
 namespace {
 
@@ -18,6 +19,8 @@ using mla::DecodeParams;
 
 constexpr int kMaxSplits = 256;
 constexpr int kB200Sms = 148;
+constexpr int kMaxTablePages = 1 << 24;           // 64 x 2^24 keys stay below 2^31
+constexpr int64_t kMaxRowStride = 1LL << 31;      // elements between two rows of a strided operand
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -63,6 +66,26 @@ WsLayout ws_layout(const mla_config_t* c, int B, int T_q, int max_splits) {
     WsLayout w;
     w.part_o = w.part_lse = w.sm100 = 256;
     w.total = w.sm100 + round256(mla::sm100_workspace_bytes(c->n_h, c->d_c, B, T_q));
+    return w;
+}
+
+// Decode of a batch behind shared pages, portable kernels: `splits` partials of
+// every row for the shared keys and as many for its own.
+int shared_splits(const mla_config_t* c, int B, int T_q, int max_splits) {
+    if (max_splits > 0) return max_splits < kMaxSplits ? max_splits : kMaxSplits;
+    const long rows = static_cast<long>(B) * T_q * c->n_h;
+    const long work = (rows + 31) / 32 + static_cast<long>(B) * T_q * ((c->n_h + 31) / 32);
+    const long s = (8L * kB200Sms + work - 1) / work;
+    return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
+}
+
+WsLayout ws_layout_shared(const mla_config_t* c, int B, int T_q, int max_splits) {
+    WsLayout w;
+    w.part_o = w.sm100 = 256;
+    const size_t parts = 2 * static_cast<size_t>(shared_splits(c, B, T_q, max_splits));
+    const size_t rows = static_cast<size_t>(B) * T_q * c->n_h;
+    w.part_lse = w.part_o + round256(parts * rows * c->d_c * 4);
+    w.total = w.part_lse + round256(parts * rows * 4);
     return w;
 }
 
@@ -467,6 +490,155 @@ int mla_decode_e4m3(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf
     P.splits = choose_splits(cfg, B, T_q, max_splits);
     P.scale_log2 = effective_scale(cfg) * mla::kLog2e;
     return cuda_rc(mla::launch_decode_simt(P, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_decode_shared_workspace_bytes(const mla_config_t* cfg, int B, int T_q, int max_splits) {
+    if (check_config(cfg) || max_splits < 0 || (cfg->impl == 2 && !mla::sm100_row_shape(cfg->d_c, cfg->d_r))) return 0;
+    if (B < 1 || T_q < 1 || static_cast<long>(B) * T_q > 65535) return 0;
+    return ws_layout_shared(cfg, B, T_q, max_splits).total;
+}
+
+int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf16* q_r,
+                      const mla_bf16* pool, int num_blocks, const int32_t* shared_table, int n_shared,
+                      const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                      int B, int T_q, int max_splits, void* workspace, size_t ws_bytes,
+                      mla_bf16* out_latent, float* out_lse, void* stream) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (cfg->impl == 2 && !mla::sm100_row_shape(cfg->d_c, cfg->d_r)) return MLA_ERR_CONFIG;
+    if (!q_abs || !q_r || !pool || !block_table || !seq_lens || !workspace || !out_latent || !out_lse)
+        return MLA_ERR_NULL;
+    if (n_shared > 0 && !shared_table) return MLA_ERR_NULL;
+    if (!aligned16(q_abs) || !aligned16(q_r) || !aligned16(pool) || !aligned16(out_latent) ||
+        !aligned4(out_lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(shared_table))
+        return MLA_ERR_ALIGN;
+    if (B < 1 || T_q < 1 || static_cast<long>(B) * T_q > 65535) return MLA_ERR_SIZE;
+    if (num_blocks < 1 || max_blocks_per_seq < 1 || max_splits < 0) return MLA_ERR_SIZE;
+    if (max_blocks_per_seq > kMaxTablePages || n_shared < 0 || n_shared > max_blocks_per_seq) return MLA_ERR_SIZE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MLA_ERR_WORKSPACE;
+    const WsLayout w = ws_layout_shared(cfg, B, T_q, max_splits);
+    if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
+
+    char* ws = static_cast<char*>(workspace);
+    DecodeParams P;
+    P.q_abs = q_abs;
+    P.q_r = q_r;
+    P.pool = pool;
+    P.block_table = block_table;
+    P.shared_table = shared_table;
+    P.n_shared = n_shared;
+    P.seq_lens = seq_lens;
+    P.out_latent = out_latent;
+    P.out_lse = out_lse;
+    P.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    P.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    P.status = reinterpret_cast<int32_t*>(ws);
+    P.n_h = cfg->n_h;
+    P.d_c = cfg->d_c;
+    P.d_r = cfg->d_r;
+    P.block_size = cfg->block_size;
+    P.num_blocks = num_blocks;
+    P.max_blocks = max_blocks_per_seq;
+    P.B = B;
+    P.T_q = T_q;
+    P.n_tok = B * T_q;
+    P.splits = shared_splits(cfg, B, T_q, max_splits);
+    P.scale_log2 = effective_scale(cfg) * mla::kLog2e;
+    return cuda_rc(mla::launch_decode_shared_simt(P, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_quantize_i8(const mla_bf16* x, int64_t ld_x, int n_rows, int d, int8_t* x8, float* scale, void* stream) {
+    if (!x || !x8 || !scale) return MLA_ERR_NULL;
+    if (!aligned16(x) || !aligned16(x8) || !aligned4(scale)) return MLA_ERR_ALIGN;
+    if (n_rows < 1 || n_rows > (1 << 24) || d < 16 || d > 65536 || d % 16) return MLA_ERR_SIZE;
+    if (ld_x < d || ld_x % 8 || ld_x > kMaxRowStride) return MLA_ERR_SIZE;
+    return cuda_rc(mla::launch_quantize_i8(x, ld_x, n_rows, d, x8, scale, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const int8_t* w8,
+                  const float* w_scale, mla_bf16* out, int n_tok, int d_in, int d_out,
+                  int32_t* dev_status, void* stream) {
+    if (!x8 || !x_scale || !w8 || !w_scale || !out) return MLA_ERR_NULL;
+    if (!aligned16(x8) || !aligned16(w8) || !aligned16(out) || !aligned4(x_scale) || !aligned4(w_scale) ||
+        (dev_status && !aligned4(dev_status)))
+        return MLA_ERR_ALIGN;
+    if (n_tok < 1 || n_tok > 65536 || d_in < 16 || d_in > 65536 || d_in % 16) return MLA_ERR_SIZE;
+    if (d_out < 8 || d_out > 131072 || d_out % 8) return MLA_ERR_SIZE;
+    if (ld_x < d_in || ld_x % 16 || ld_x > kMaxRowStride) return MLA_ERR_SIZE;
+    if (mla_check_device() != MLA_OK) return MLA_ERR_UNSUPPORTED;
+    return cuda_rc(mla::launch_linear_i8(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, dev_status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int mla_block_norm(const mla_bf16* u, int64_t ld_u, const mla_bf16* w_post, const mla_bf16* gate,
+                   int64_t ld_gate, float alpha, const mla_bf16* residual, mla_bf16* residual_out,
+                   const mla_bf16* w_pre, float eps, int n_tok, int d, mla_bf16* out, int8_t* out8,
+                   float* out8_scale, void* stream) {
+    if (!u || (!residual_out && !out && !out8)) return MLA_ERR_NULL;
+    if (residual_out && !residual) return MLA_ERR_NULL;
+    if (!w_pre != (!out && !out8) || !out8 != !out8_scale) return MLA_ERR_NULL;
+    if (!aligned16(u) || !aligned16(w_post) || !aligned16(gate) || !aligned16(residual) ||
+        !aligned16(residual_out) || !aligned16(w_pre) || !aligned16(out) || !aligned16(out8) ||
+        !aligned4(out8_scale))
+        return MLA_ERR_ALIGN;
+    if (n_tok < 1 || n_tok > (1 << 24) || d < 8 || d > 16384 || d % 8 || (out8 && d % 16)) return MLA_ERR_SIZE;
+    if (ld_u < d || ld_u % 8 || ld_u > kMaxRowStride) return MLA_ERR_SIZE;
+    if (gate && ld_gate != 0 && (ld_gate < d || ld_gate % 8 || ld_gate > kMaxRowStride)) return MLA_ERR_SIZE;
+    if (!(eps > 0.f) || !isfinite(eps) || !isfinite(alpha)) return MLA_ERR_SIZE;
+    mla::BlockNormArgs a;
+    a.u = u, a.w_post = w_post, a.gate = gate, a.residual = residual, a.w_pre = w_pre;
+    a.residual_out = residual_out, a.out = out, a.out8 = out8, a.out8_scale = out8_scale;
+    a.ld_u = ld_u, a.ld_gate = ld_gate, a.alpha = alpha, a.eps = eps, a.n_tok = n_tok, a.d = d;
+    return cuda_rc(mla::launch_block_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int norm_rope_append(const mla_config_t* cfg, const mla_bf16* q, const mla_bf16* kv, int64_t ld_kv,
+                     const mla_bf16* w_kv, float eps, const int32_t* positions, const float* rope_table, int max_pos,
+                     const int32_t* block_table, int max_blocks_per_seq, void* pool, bool e4m3, int num_blocks, int B,
+                     int T_q, mla_bf16* q_c, mla_bf16* q_r, int32_t* dev_status, void* stream) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (e4m3 && !e4m3_shape(cfg)) return MLA_ERR_CONFIG;
+    if (!kv || !w_kv || !positions || !rope_table || !block_table || !pool) return MLA_ERR_NULL;
+    if (!q != !q_c || !q != !q_r) return MLA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(q_c) || !aligned16(q_r) || !aligned16(kv) || !aligned16(w_kv) ||
+        !aligned16(pool) || !aligned16(rope_table))
+        return MLA_ERR_ALIGN;
+    if (!aligned4(positions) || !aligned4(block_table) || (dev_status && !aligned4(dev_status))) return MLA_ERR_ALIGN;
+    if (B < 1 || T_q < 1 || static_cast<long>(B) * T_q > (1L << 24)) return MLA_ERR_SIZE;
+    if (max_pos < 1 || max_blocks_per_seq < 1 || num_blocks < 1) return MLA_ERR_SIZE;
+    if (ld_kv < cfg->d_c + cfg->d_r || ld_kv % 8 || ld_kv > kMaxRowStride) return MLA_ERR_SIZE;
+    if (!(eps > 0.f) || !isfinite(eps)) return MLA_ERR_SIZE;
+    return cuda_rc(mla::launch_norm_rope_append(q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
+                                                max_blocks_per_seq, pool, e4m3, num_blocks, B * T_q, T_q, cfg->n_h,
+                                                cfg->d_c, cfg->d_h, cfg->d_r, cfg->block_size, q_c, q_r, dev_status,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_norm_rope_append(const mla_config_t* cfg, const mla_bf16* q, const mla_bf16* kv, int64_t ld_kv,
+                         const mla_bf16* w_kv, float eps, const int32_t* positions,
+                         const float* rope_table, int max_pos, const int32_t* block_table,
+                         int max_blocks_per_seq, mla_bf16* pool, int num_blocks, int B, int T_q,
+                         mla_bf16* q_c, mla_bf16* q_r, int32_t* dev_status, void* stream) {
+    return norm_rope_append(cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
+                            max_blocks_per_seq, pool, false, num_blocks, B, T_q, q_c, q_r, dev_status, stream);
+}
+
+int mla_norm_rope_append_e4m3(const mla_config_t* cfg, const mla_bf16* q, const mla_bf16* kv,
+                              int64_t ld_kv, const mla_bf16* w_kv, float eps, const int32_t* positions,
+                              const float* rope_table, int max_pos, const int32_t* block_table,
+                              int max_blocks_per_seq, uint8_t* pool, int num_blocks, int B, int T_q,
+                              mla_bf16* q_c, mla_bf16* q_r, int32_t* dev_status, void* stream) {
+    return norm_rope_append(cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
+                            max_blocks_per_seq, pool, true, num_blocks, B, T_q, q_c, q_r, dev_status, stream);
 }
 
 int mla_clear_status(int32_t* dev_status, void* stream) {

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "layer.h"
 
 namespace mla {
 
@@ -36,18 +37,8 @@ __device__ __forceinline__ void rope_pair(uint16_t x1b, uint16_t x2b, float c, f
 // One warp quantises a latent row of d_c <= 512 values: lane l takes values
 // 16 l .. 16 l + 15, four lanes make a 64-column group.  All 32 lanes take
 // part in the group maxima (lanes past d_c / 16 hold zeros).
-__device__ __forceinline__ void quantize_row_e4m3(const uint16_t* __restrict__ src, unsigned char* row, int d_c,
-                                                  int scale_off, int lane) {
-    const bool active = 16 * lane < d_c;
-    float x[16];
-    if (active) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + 16 * lane);
-        unpack8(s4[0], x);
-        unpack8(s4[1], x + 8);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = 0.f;
-    }
+__device__ __forceinline__ void quantize_values_e4m3(const float (&x)[16], bool active, unsigned char* row,
+                                                     int scale_off, int lane) {
     float amax = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
@@ -65,6 +56,27 @@ __device__ __forceinline__ void quantize_row_e4m3(const uint16_t* __restrict__ s
     *reinterpret_cast<uint4*>(row + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
     if ((lane & 3) == 0)
         *reinterpret_cast<float*>(row + scale_off + 4 * (lane >> 2)) = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
+}
+
+__device__ __forceinline__ void quantize_row_e4m3(const uint16_t* __restrict__ src, unsigned char* row, int d_c,
+                                                  int scale_off, int lane) {
+    const bool active = 16 * lane < d_c;
+    float x[16];
+    if (active) {
+        const uint4* s4 = reinterpret_cast<const uint4*>(src + 16 * lane);
+        unpack8(s4[0], x);
+        unpack8(s4[1], x + 8);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = 0.f;
+    }
+    quantize_values_e4m3(x, active, row, scale_off, lane);
+}
+
+// The zero padding of an e4m3 row.
+__device__ __forceinline__ void pad_row_e4m3(unsigned char* row, const E4m3Row& L, int d_c, int d_r, int lane) {
+    for (int o = L.scale_off + 4 * (d_c / MLA_E4M3_GROUP) + lane; o < L.kr_off; o += 32) row[o] = 0;
+    for (int o = L.kr_off + 2 * d_r + lane; o < L.bytes; o += 32) row[o] = 0;
 }
 
 // kE4m3: the pool holds e4m3 rows (row_bytes each, scales at scale_off, the
@@ -135,9 +147,7 @@ rope_append_kernel(uint16_t* __restrict__ q_r, const uint16_t* __restrict__ k_r,
         const E4m3Row L = e4m3_row(d_c, d_r);
         unsigned char* row = pool + slot * L.bytes;
         quantize_row_e4m3(c_kv + static_cast<size_t>(n) * d_c, row, d_c, L.scale_off, lane);
-        // padding bytes are zero
-        for (int o = L.scale_off + 4 * (d_c / MLA_E4M3_GROUP) + lane; o < L.kr_off; o += 32) row[o] = 0;
-        for (int o = L.kr_off + 2 * d_r + lane; o < L.bytes; o += 32) row[o] = 0;
+        pad_row_e4m3(row, L, d_c, d_r, lane);
         key = reinterpret_cast<uint16_t*>(row + L.kr_off);
     } else {
         uint16_t* row = reinterpret_cast<uint16_t*>(pool) + slot * (d_c + d_r);
@@ -174,6 +184,157 @@ cudaError_t launch_rope_append(uint16_t* q_r, const uint16_t* k_r, const uint16_
     return launch_pdl(rope_append_kernel<false>, grid, dim3(threads), 0, stream, q_r, k_r, c_kv, positions, table,
                       max_pos, block_table, max_blocks, p, num_blocks, n_tok, T_q, n_h, d_c, d_r, block_size,
                       static_cast<int>(q_blocks), status);
+}
+
+// mla_norm_rope_append: the append from the projections' rows.  The same two
+// kinds of blocks: [0, q_blocks) split the query rows (n_h, d_h + d_r), a
+// thread per 8 values -- a copy into q_c, or four rotated pairs into q_r -- and
+// the rest append, one warp per token: a lane holds 16 latent values, the sum
+// of squares is a warp reduction, and the key is rotated as above.  Bound by
+// memory: every byte read once and written once.
+struct NormAppendArgs {
+    const uint16_t* q;
+    const uint16_t* kv;
+    const uint16_t* w_kv;
+    const int32_t* positions;
+    const float* table;
+    const int32_t* block_table;
+    unsigned char* pool;
+    uint16_t* q_c;
+    uint16_t* q_r;
+    int32_t* status;
+    long ld_kv;
+    float eps;
+    int max_pos, max_blocks, num_blocks, n_tok, T_q, n_h, d_c, d_h, d_r, block_size, q_blocks;
+};
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(256) norm_rope_append_kernel(const NormAppendArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();   // the projections, the pool and the outputs may be in use by earlier kernels
+    const int h = a.d_r >> 1;
+    if (static_cast<int>(blockIdx.x) < a.q_blocks) {
+        const int copies = a.d_h >> 3, items = copies + (a.d_r >> 3);
+        const long g = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+        if (g >= static_cast<long>(a.n_tok) * a.n_h * items) return;
+        const long ni = g / items;                      // token * n_h + head
+        const int item = static_cast<int>(g - ni * items);
+        const int n = static_cast<int>(ni / a.n_h);
+        const int p = a.positions[n];
+        if (p < 0 || p >= a.max_pos || p / a.block_size >= a.max_blocks) return;   // flagged by the append
+        const uint16_t* src = a.q + ni * (a.d_h + a.d_r);
+        if (item < copies) {
+            reinterpret_cast<uint4*>(a.q_c + ni * a.d_h)[item] = reinterpret_cast<const uint4*>(src)[item];
+            return;
+        }
+        src += a.d_h;
+        const int m = 4 * (item - copies);
+        const float4 c = *reinterpret_cast<const float4*>(a.table + static_cast<size_t>(p) * a.d_r + m);
+        const float4 sn = *reinterpret_cast<const float4*>(a.table + static_cast<size_t>(p) * a.d_r + h + m);
+        const uint2 x1 = *reinterpret_cast<const uint2*>(src + m);
+        const uint2 x2 = *reinterpret_cast<const uint2*>(src + h + m);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+        const uint32_t a_in[2] = {x1.x, x1.y}, b_in[2] = {x2.x, x2.y};
+        uint32_t a_out[2], b_out[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint16_t y1[2], y2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                rope_pair(static_cast<uint16_t>(a_in[w] >> (16 * e)), static_cast<uint16_t>(b_in[w] >> (16 * e)),
+                          cc[2 * w + e], ss[2 * w + e], &y1[e], &y2[e]);
+            a_out[w] = y1[0] | (static_cast<uint32_t>(y1[1]) << 16);
+            b_out[w] = y2[0] | (static_cast<uint32_t>(y2[1]) << 16);
+        }
+        uint16_t* dst = a.q_r + ni * a.d_r;
+        *reinterpret_cast<uint2*>(dst + m) = make_uint2(a_out[0], a_out[1]);
+        *reinterpret_cast<uint2*>(dst + h + m) = make_uint2(b_out[0], b_out[1]);
+        return;
+    }
+
+    const int n = (blockIdx.x - a.q_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (n >= a.n_tok) return;
+    const int b = n / a.T_q;
+    const int p = a.positions[n];
+    if (p < 0 || p >= a.max_pos || p / a.block_size >= a.max_blocks) {
+        if (lane == 0) raise_status(a.status, MLA_STATUS_BAD_POSITION);
+        return;
+    }
+    const int blk = a.block_table[static_cast<size_t>(b) * a.max_blocks + p / a.block_size];
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (lane == 0) raise_status(a.status, MLA_STATUS_BAD_BLOCK);
+        return;
+    }
+    const size_t slot = static_cast<size_t>(blk) * a.block_size + (p % a.block_size);
+    const uint16_t* src = a.kv + n * a.ld_kv;
+
+    // 16 consecutive latent values per lane (vectors 2 lane, 2 lane + 1)
+    const int nv = a.d_c >> 3;
+    float x[16], w[16];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int j = 2 * lane + k;
+        if (j < nv) {
+            unpack8(reinterpret_cast<const uint4*>(src)[j], x + 8 * k);
+            unpack8(reinterpret_cast<const uint4*>(a.w_kv)[j], w + 8 * k);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 * k + e] = w[8 * k + e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[8 * k + e], x[8 * k + e], s);
+    }
+    const float rstd = rsqrtf(warp_sum(s) / static_cast<float>(a.d_c) + a.eps);
+    uint32_t y[8];   // the normed latent, rounded once to bf16
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[2 * k] * rstd * w[2 * k], x[2 * k + 1] * rstd * w[2 * k + 1]);
+    uint16_t* key;
+    if constexpr (kE4m3) {
+        const E4m3Row L = e4m3_row(a.d_c, a.d_r);
+        unsigned char* row = a.pool + slot * L.bytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            x[2 * k] = __uint_as_float(y[k] << 16);
+            x[2 * k + 1] = __uint_as_float(y[k] & 0xFFFF0000u);
+        }
+        quantize_values_e4m3(x, 16 * lane < a.d_c, row, L.scale_off, lane);
+        pad_row_e4m3(row, L, a.d_c, a.d_r, lane);
+        key = reinterpret_cast<uint16_t*>(row + L.kr_off);
+    } else {
+        uint16_t* row = reinterpret_cast<uint16_t*>(a.pool) + slot * (a.d_c + a.d_r);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (2 * lane + k < nv)
+                reinterpret_cast<uint4*>(row)[2 * lane + k] =
+                    make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        key = row + a.d_c;
+    }
+    const float* cs = a.table + static_cast<size_t>(p) * a.d_r;
+    const uint16_t* kr = src + a.d_c;
+    for (int m = lane; m < h; m += 32) rope_pair(kr[m], kr[m + h], cs[m], cs[h + m], &key[m], &key[m + h]);
+}
+
+cudaError_t launch_norm_rope_append(const uint16_t* q, const uint16_t* kv, long ld_kv, const uint16_t* w_kv, float eps,
+                                    const int32_t* positions, const float* table, int max_pos,
+                                    const int32_t* block_table, int max_blocks, void* pool, bool e4m3, int num_blocks,
+                                    int n_tok, int T_q, int n_h, int d_c, int d_h, int d_r, int block_size,
+                                    uint16_t* q_c, uint16_t* q_r, int32_t* status, cudaStream_t stream) {
+    const int threads = 256, warps = threads / 32;
+    const long q_threads = q != nullptr ? static_cast<long>(n_tok) * n_h * ((d_h + d_r) / 8) : 0;
+    const long q_blocks = (q_threads + threads - 1) / threads;
+    const long a_blocks = (n_tok + warps - 1) / warps;
+    if (q_blocks + a_blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+    NormAppendArgs a;
+    a.q = q, a.kv = kv, a.w_kv = w_kv, a.positions = positions, a.table = table, a.block_table = block_table;
+    a.pool = static_cast<unsigned char*>(pool), a.q_c = q_c, a.q_r = q_r, a.status = status;
+    a.ld_kv = ld_kv, a.eps = eps, a.max_pos = max_pos, a.max_blocks = max_blocks, a.num_blocks = num_blocks;
+    a.n_tok = n_tok, a.T_q = T_q, a.n_h = n_h, a.d_c = d_c, a.d_h = d_h, a.d_r = d_r, a.block_size = block_size;
+    a.q_blocks = static_cast<int>(q_blocks);
+    const dim3 grid(static_cast<unsigned>(q_blocks + a_blocks));
+    return launch_pdl(e4m3 ? norm_rope_append_kernel<true> : norm_rope_append_kernel<false>, grid, dim3(threads), 0,
+                      stream, a);
 }
 
 }  // namespace mla

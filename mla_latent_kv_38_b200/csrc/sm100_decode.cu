@@ -1289,6 +1289,8 @@ std::atomic<uint64_t> g_test_wait_limit_ns{0};
 
 }  // namespace
 
+bool sm100_row_shape(int d_c, int d_r) { return d_c == kDc && d_r == kDr; }
+
 bool sm100_supports(int n_h, int d_c, int d_r) { return d_c == kDc && d_r == kDr && n_h % 128 == 0; }
 
 size_t sm100_workspace_bytes(int n_h, int d_c, int B, int T_q) {

@@ -9,6 +9,8 @@ namespace mla {
 
 struct DecodeParams;
 
+// The cache row that the tcgen05 decode kernels are built for.
+bool sm100_row_shape(int d_c, int d_r);
 bool sm100_supports(int n_h, int d_c, int d_r);
 size_t sm100_workspace_bytes(int n_h, int d_c, int B, int T_q);
 int sm100_launches(int B, int T_q, int n_h);
