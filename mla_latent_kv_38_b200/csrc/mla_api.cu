@@ -79,9 +79,18 @@ int shared_splits(const mla_config_t* c, int B, int T_q, int max_splits) {
     return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
+bool shared_uses_sm100(const mla_config_t* c) {
+    return c->impl != 1 && mla::sm100_row_shape(c->d_c, c->d_r);
+}
+
 WsLayout ws_layout_shared(const mla_config_t* c, int B, int T_q, int max_splits) {
     WsLayout w;
     w.part_o = w.sm100 = 256;
+    if (shared_uses_sm100(c)) {
+        w.part_lse = 256;
+        w.total = w.sm100 + round256(mla::sm100_shared_workspace_bytes(c->n_h, B, T_q));
+        return w;
+    }
     const size_t parts = 2 * static_cast<size_t>(shared_splits(c, B, T_q, max_splits));
     const size_t rows = static_cast<size_t>(B) * T_q * c->n_h;
     w.part_lse = w.part_o + round256(parts * rows * c->d_c * 4);
@@ -516,6 +525,10 @@ int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_
     if (num_blocks < 1 || max_blocks_per_seq < 1 || max_splits < 0) return MLA_ERR_SIZE;
     if (max_blocks_per_seq > kMaxTablePages || n_shared < 0 || n_shared > max_blocks_per_seq) return MLA_ERR_SIZE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MLA_ERR_WORKSPACE;
+    const bool sm100 = shared_uses_sm100(cfg);
+    // the tcgen05 kernels number the pages of all units of work in 32 bits
+    if (sm100 && static_cast<int64_t>(B) * T_q * ((cfg->n_h + 127) / 128) * max_blocks_per_seq >= (1LL << 29))
+        return MLA_ERR_SIZE;
     const WsLayout w = ws_layout_shared(cfg, B, T_q, max_splits);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
 
@@ -544,6 +557,10 @@ int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_
     P.n_tok = B * T_q;
     P.splits = shared_splits(cfg, B, T_q, max_splits);
     P.scale_log2 = effective_scale(cfg) * mla::kLog2e;
+    if (sm100) {
+        if (mla_check_device() != MLA_OK) return MLA_ERR_UNSUPPORTED;
+        return cuda_rc(mla::launch_decode_shared_sm100(P, ws + w.sm100, max_splits, static_cast<cudaStream_t>(stream)));
+    }
     return cuda_rc(mla::launch_decode_shared_simt(P, static_cast<cudaStream_t>(stream)));
 }
 

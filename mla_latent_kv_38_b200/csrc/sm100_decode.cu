@@ -132,6 +132,17 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, 256, 0, 1);
 constexpr uint32_t kSuspendHintNs = 100000;      // a waiting thread sleeps up to 0.1 ms per try
 constexpr float kRescaleThreshold = 8.0f;         // log2 units
 
+// How the query rows are cut into units of work (described at unit_keys).
+struct UnitMap {
+    int n_h, n_hb, B, T_q, max_blocks;
+    // the shared decode only:
+    int n_shared;      // pages that every sequence begins with
+    int n_prefix;      // units of the shared keys; 0: every unit walks the shared pages, then its own
+    int n_rows;        // query rows of the batch
+    int tok_per_unit;  // whole tokens of a sequence in one unit (1 when n_h > 64)
+    int own_rows;      // rows of a sequence unit's partial slot, a multiple of 32
+};
+
 struct Sm100Params {
     CUtensorMap tm_pool;      // pool as [rows][576], box 64 cols x 64 rows
     CUtensorMap tm_pool_v;    // pool as [chunk][rows][64], box 64 cols x 64 rows x 4 chunks
@@ -151,12 +162,21 @@ struct Sm100Params {
     float* part_o;            // (C + U) slots x 128 rows x 512
     float* part_lse;          // (C + U) slots x 128
     int32_t* status;
-    int n_h, n_hb, B, T_q, U, num_blocks, max_blocks, max_splits;
+    const int32_t* shared_table;   // (n_shared) blocks of the shared pages (shared decode only)
+    UnitMap um;
+    int U, num_blocks, max_splits;
     int in_kernel_schedule;   // 1: each CTA computes the schedule; 0: the schedule kernel did
     int withhold_load;        // test hook: 1 = never issue the first S entry's load of CTA 0
     uint64_t timeout_ns;      // bound of every wait
     float scale_log2;
 };
+
+// Two bf16 values with infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+    return v;
+}
 
 __device__ __forceinline__ bool wait_bar(uint32_t addr, uint32_t parity, volatile int* abort_flag,
                                          int32_t* status, uint64_t timeout_ns) {
@@ -184,6 +204,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t addr, uint32_t parity, volatil
 // is out of range has no pages (its outputs are defined as zero / -inf by
 // the merge kernel).  pf is the exclusive prefix of the page counts, T =
 // pf[U] the total.
+//
+// Shared decode (kShared).  A unit of a sequence takes as many whole tokens as
+// fit its 128 rows (tok_per_unit, at most 64; t then counts such groups); a
+// token's row sees kv minus the tokens behind it in the unit.  The shared
+// pages are either walked by every sequence unit in front of its own
+// (n_prefix = 0), or by n_prefix units of their own in front of the others:
+// 128 consecutive query rows of the whole batch, whatever their sequence.
+// The sequence units then begin behind the shared pages.
 // ---------------------------------------------------------------------------
 
 struct UnitIdx {
@@ -196,10 +224,27 @@ __device__ __forceinline__ UnitIdx unit_index(int u, int n_hb, int B) {
     return UnitIdx{r - t * B, t, u - r * n_hb};
 }
 
-__device__ __forceinline__ int unit_keys(const int32_t* seq_lens, int u, int n_hb, int B, int T_q, int max_blocks) {
-    const UnitIdx x = unit_index(u, n_hb, B);
-    const int L = seq_lens[x.b];   // global or shared memory
-    return (L >= T_q && L <= max_blocks * kPage) ? L - T_q + x.t + 1 : 0;
+template <bool kShared>
+__device__ __forceinline__ int unit_keys(const int32_t* seq_lens, int u, const UnitMap& um) {
+    if constexpr (kShared) {
+        const int own0 = um.n_shared * kPage;
+        if (u < um.n_prefix) return own0;
+        const UnitIdx x = unit_index(u - um.n_prefix, um.n_hb, um.B);
+        const int L = seq_lens[x.b];
+        if (L - own0 < um.T_q || L > um.max_blocks * kPage) return 0;
+        return L - um.T_q + min(um.T_q, (x.t + 1) * um.tok_per_unit) - (um.n_prefix > 0 ? own0 : 0);
+    } else {
+        const UnitIdx x = unit_index(u, um.n_hb, um.B);
+        const int L = seq_lens[x.b];   // global or shared memory
+        return (L >= um.T_q && L <= um.max_blocks * kPage) ? L - um.T_q + x.t + 1 : 0;
+    }
+}
+
+// Whether u is the first unit of a sequence (the one that reports its length).
+template <bool kShared>
+__device__ __forceinline__ bool first_of_sequence(int u, const UnitMap& um) {
+    if constexpr (kShared) u -= um.n_prefix;
+    return u >= 0 && u < um.B * um.n_hb && u % um.n_hb == 0;
 }
 
 // Last unit v with pf[v] <= g (for g < T: the unit holding page g).
@@ -299,10 +344,10 @@ __device__ int cluster_of_page(int g, const int* cuts) {
 }
 
 // Merge metadata of unit u: {kv_len, first cluster, parts, sequence}.
-__device__ int4 unit_meta_of(int u, const int32_t* pf, const int* cuts, const int32_t* seq_lens, int n_hb, int B,
-                             int T_q, int max_blocks) {
-    const int kv = unit_keys(seq_lens, u, n_hb, B, T_q, max_blocks);
-    const int b = unit_index(u, n_hb, B).b;
+template <bool kShared>
+__device__ int4 unit_meta_of(int u, const int32_t* pf, const int* cuts, const int32_t* seq_lens, const UnitMap& um) {
+    const int kv = unit_keys<kShared>(seq_lens, u, um);
+    const int b = kShared ? 0 : unit_index(u, um.n_hb, um.B).b;
     const int a = pf[u], e = pf[u + 1];
     if (e <= a) return make_int4(0, 0, 0, b);
     const int c0 = cluster_of_page(a, cuts);
@@ -312,11 +357,12 @@ __device__ int4 unit_meta_of(int u, const int32_t* pf, const int* cuts, const in
 
 // One tile of a cluster's work: up to 4 consecutive pages of one unit.
 struct Tile {
-    int u;          // unit = (t B + b) n_hb + hb
-    int bt;         // query row b T_q + t of the unit
-    int hb;         // head block of the unit
+    int u;          // unit = (t B + b) n_hb + hb (behind the prefix units)
+    int row0;       // first query row of the unit (bt n_h + 128 hb)
+    int rows;       // query rows of the unit (128 but in the shared decode)
+    int n_tok;      // tokens of the unit (1 but in the shared decode)
     int b;          // sequence of the unit
-    int kv;         // keys of the unit (kv_len)
+    int kv;         // keys of the unit (kv_len; of its last token)
     int page0;      // first page, within the unit
     int np;         // pages in this tile (1..4)
     bool first;     // first tile of a unit segment (new query, O starts from zero)
@@ -325,14 +371,24 @@ struct Tile {
     bool whole;     // the whole unit lies in this cluster's range (no partial)
 };
 
+// Page pg of the tile holds rows that not every token of the unit sees, or
+// that lie behind the last key: its V rows are cleaned before they are used.
+template <bool kShared>
+__device__ __forceinline__ bool tail_page(const Tile& t, int pg) {
+    if constexpr (kShared) return kPage * (t.page0 + pg + 1) > t.kv - (t.n_tok - 1);
+    return t.unit_end && (t.kv % kPage) != 0 && pg == t.np - 1;
+}
+
 // Walks a cluster's pages [g0, g1) as tiles.  kvs[v - off] is the key count
 // of unit v (a shared-memory slice of the cluster's units, or a global array
 // with off = 0); unit u0 starts at global page ubeg0.  The unit's page range
 // and (query row, head block, sequence) are kept up to date incrementally.
+template <bool kShared>
 struct TileWalker {
     const int32_t* kvs;
     int off, g, g0, g1, u, ubeg, uend, kv;
-    int bt, hb, b, t, n_hb, B, T_q;
+    int bt, hb, b, t, n_h, n_hb, B, T_q;
+    int n_prefix, n_rows, per;   // kShared only
     __device__ void load_unit() {
         kv = kvs[u - off];
         uend = ubeg + (kv + kPage - 1) / kPage;
@@ -341,28 +397,34 @@ struct TileWalker {
         ++u;
         ubeg = uend;
         load_unit();
+        if (kShared && u <= n_prefix) return;   // the first sequence unit is (0, 0, 0), set by init
         if (++hb == n_hb) {
             hb = 0;
             if (++b == B) {
                 b = 0;
                 ++t;
             }
-            bt = b * T_q + t;
+            if (!kShared) bt = b * T_q + t;
         }
     }
-    __device__ void init(const int32_t* kvs_, int off_, int u0, int ubeg0, int g0_, int g1_, int n_hb_, int B_,
-                         int T_q_) {
+    __device__ void init(const int32_t* kvs_, int off_, int u0, int ubeg0, int g0_, int g1_, const UnitMap& um) {
         kvs = kvs_;
         off = off_;
         g = g0_;
         g0 = g0_;
         g1 = g1_;
-        n_hb = n_hb_;
-        B = B_;
-        T_q = T_q_;
+        n_h = um.n_h;
+        n_hb = um.n_hb;
+        B = um.B;
+        T_q = um.T_q;
         u = u0;
         ubeg = ubeg0;
-        const UnitIdx x = unit_index(u0, n_hb, B);
+        if constexpr (kShared) {
+            n_prefix = um.n_prefix;
+            n_rows = um.n_rows;
+            per = um.tok_per_unit;
+        }
+        const UnitIdx x = unit_index(kShared ? max(u0 - n_prefix, 0) : u0, n_hb, B);
         b = x.b;
         t = x.t;
         hb = x.hb;
@@ -376,8 +438,21 @@ struct TileWalker {
     __device__ Tile next() {
         Tile r;
         r.u = u;
-        r.bt = bt;
-        r.hb = hb;
+        if constexpr (kShared) {
+            if (u < n_prefix) {
+                r.row0 = 128 * u;
+                r.rows = min(128, n_rows - r.row0);
+                r.n_tok = 1;
+            } else {
+                r.n_tok = min(per, T_q - t * per);
+                r.row0 = (b * T_q + t * per) * n_h + 128 * hb;
+                r.rows = per > 1 ? r.n_tok * n_h : min(128, n_h - 128 * hb);
+            }
+        } else {
+            r.row0 = bt * n_h + hb * 128;
+            r.rows = 128;
+            r.n_tok = 1;
+        }
         r.b = b;
         r.kv = kv;
         r.page0 = g - ubeg;
@@ -396,14 +471,15 @@ struct TileWalker {
 // Block-wide exclusive scans of the units' page counts, tile counts and cut
 // costs into pf, tf, wf[0 .. U] (U <= kInKernelUnits); every thread of the
 // CTA takes part; warp_tot holds 3 x 16 ints of scratch.  Returns {T, Tt}.
-__device__ int2 schedule_scan(int* pf, int* tf, int* wf, int* warp_tot, const int32_t* seq_lens, int U, int n_hb,
-                              int B, int T_q, int max_blocks) {
+template <bool kShared>
+__device__ int2 schedule_scan(int* pf, int* tf, int* wf, int* warp_tot, const int32_t* seq_lens, int U,
+                              const UnitMap& um) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int per = (U + kThreads - 1) / kThreads;
     const int beg = min(U, tid * per), end = min(U, beg + per);
     int loc[3] = {0, 0, 0};
     for (int u = beg; u < end; ++u) {
-        const int pages = (unit_keys(seq_lens, u, n_hb, B, T_q, max_blocks) + kPage - 1) / kPage;
+        const int pages = (unit_keys<kShared>(seq_lens, u, um) + kPage - 1) / kPage;
         const int tiles = (pages + kTilePages - 1) / kTilePages;
         pf[u + 1] = pages;
         tf[u + 1] = tiles;
@@ -452,11 +528,19 @@ __device__ int2 schedule_scan(int* pf, int* tf, int* wf, int* warp_tot, const in
     return make_int2(pf[U], tf[U]);
 }
 
+// First partial row of sequence unit uo (counted behind the prefix units) in
+// cluster c: the slots of the prefix units, 128 rows each, come first.
+__device__ __forceinline__ size_t own_slot_row(int c, int uo, const UnitMap& um) {
+    const size_t base = um.n_prefix > 0 ? static_cast<size_t>(kClusters + um.n_prefix) * 128 : 0;
+    return base + (static_cast<size_t>(c) + uo) * um.own_rows;
+}
+
 // P.V operand split: CTA r supplies latent chunks 4r .. 4r+3 (columns
 // [256r, 256r+256)); instruction h (N = 256) takes chunks 4r+2h, 4r+2h+1 from
 // each CTA, so TMEM column 128h + j of lane half r holds latent column
 // 256r + 128h + j.  V ring entry (page, h) holds exactly those two chunks.
 
+template <bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -519,8 +603,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
     if (warp >= 4) {
         const char* lens_b = reinterpret_cast<const char*>(p.seq_lens);
         const char* tab_b = reinterpret_cast<const char*>(p.block_table);
-        const long n_lens = (static_cast<long>(p.B) * 4 + 127) / 128;
-        const long n_tab = (static_cast<long>(p.B) * p.max_blocks * 4 + 127) / 128;
+        const long n_lens = (static_cast<long>(p.um.B) * 4 + 127) / 128;
+        const long n_tab = (static_cast<long>(p.um.B) * p.um.max_blocks * 4 + 127) / 128;
         for (long k = blockIdx.x + static_cast<long>(gridDim.x) * (threadIdx.x - 128); k < n_lens + n_tab;
              k += static_cast<long>(gridDim.x) * (kThreads - 128))
             ptx::prefetch_l2_line(k < n_lens ? lens_b + 128 * k : tab_b + 128 * (k - n_lens));
@@ -544,9 +628,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         int* ctmp = wfx + kInKernelUnits + 1;                         // cut scratch, C + 1
         int* lens = ctmp + kClusters + 1;                             // sequence lengths, B <= U
         int* wtot = lens + kInKernelUnits;                            // scan scratch, 48
-        for (int b = threadIdx.x; b < p.B; b += kThreads) lens[b] = __ldg(p.seq_lens + b);
+        for (int b = threadIdx.x; b < p.um.B; b += kThreads) lens[b] = __ldg(p.seq_lens + b);
         __syncthreads();
-        const int2 TT = schedule_scan(sc, tfx, wfx, wtot, lens, p.U, p.n_hb, p.B, p.T_q, p.max_blocks);
+        const int2 TT = schedule_scan<kShared>(sc, tfx, wfx, wtot, lens, p.U, p.um);
         const int T = TT.x;
         int* cuts = reinterpret_cast<int*>(smem + kOffCuts);
         compute_cuts(cuts, ctmp, sc, tfx, wfx, p.U, T, TT.y, p.max_splits);
@@ -562,14 +646,14 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 kv_base = dst;
             }
             for (int k = threadIdx.x; k <= u1 - u0; k += kThreads)
-                dst[k] = unit_keys(lens, u0 + k, p.n_hb, p.B, p.T_q, p.max_blocks);
+                dst[k] = unit_keys<kShared>(lens, u0 + k, p.um);
         }
         kv_off = u0;
         // merge metadata and length checks, spread over the grid's threads
         for (int u = blockIdx.x * kThreads + threadIdx.x; u < p.U; u += gridDim.x * kThreads) {
-            const int4 m = unit_meta_of(u, sc, cuts, lens, p.n_hb, p.B, p.T_q, p.max_blocks);
+            const int4 m = unit_meta_of<kShared>(u, sc, cuts, lens, p.um);
             p.unit_meta[u] = m;
-            if (m.x == 0 && u < p.B * p.n_hb && u % p.n_hb == 0) raise_status(p.status, MLA_STATUS_BAD_SEQ_LEN);
+            if (m.x == 0 && first_of_sequence<kShared>(u, p.um)) raise_status(p.status, MLA_STATUS_BAD_SEQ_LEN);
         }
     } else {
         const int4 cinfo = p.cluster_info[cluster];
@@ -596,7 +680,13 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
     // ring waits of the tiles in between; an entry is validated where it is
     // used (out-of-range entries are flagged and read as block 0).
     auto load_blk = [&](const Tile& t, int pg) -> int {
-        return __ldg(p.block_table + static_cast<size_t>(t.b) * p.max_blocks + t.page0 + pg);
+        int page = t.page0 + pg;
+        if constexpr (kShared) {
+            const bool prefix = t.u < p.um.n_prefix;
+            if (prefix || (p.um.n_prefix == 0 && page < p.um.n_shared)) return __ldg(p.shared_table + page);
+            if (p.um.n_prefix > 0) page += p.um.n_shared;
+        }
+        return __ldg(p.block_table + static_cast<size_t>(t.b) * p.um.max_blocks + page);
     };
     auto blk_row = [&](int blk) -> int {
         if (blk < 0 || blk >= p.num_blocks) {
@@ -605,7 +695,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         }
         return blk * kPage;
     };
-    auto walker = [&](TileWalker& w) { w.init(kv_base, kv_off, u0, ubeg0, g0, g1, p.n_hb, p.B, p.T_q); };
+    auto walker = [&](TileWalker<kShared>& w) { w.init(kv_base, kv_off, u0, ubeg0, g0, g1, p.um); };
 
     if (warp < 4) {
         // Warpgroup 0 (loads and MMA issue) needs few registers: it gives them to
@@ -627,7 +717,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             const int grp = lane >> 2, j = lane & 3;
             const bool active = grp < kSLaneGroups && j < 3;
             const int my_pg = 2 * static_cast<int>(rank) + (j & 1);
-            TileWalker w, wa;
+            TileWalker<kShared> w, wa;
             walker(w);
             walker(wa);
             int b0 = 0, b1 = 0, b2 = 0;
@@ -649,7 +739,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             bool ok = g0 < g1;
             while (ok && !w.done()) {
                 const Tile cur = w.next();
-                const int qrow = cur.bt * p.n_h + cur.hb * 128 + 64 * static_cast<int>(rank);
+                const int qrow = cur.row0 + 64 * static_cast<int>(rank);
                 const int row = h0 ? blk_row(b0) : 0;
                 const uint32_t tx = static_cast<uint32_t>(cur.np + 2) * kBox;    // both CTAs' page and query chunks
                 for (int c = 0; c < kChunks; ++c, ++e) {
@@ -680,7 +770,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             // different threads.  Lane pg < 4 holds the block of page pg of the
             // current tile (v0) and of the next one (v1).
             const uint64_t pol_v = ptx::l2_policy_evict_first();   // last use of these lines
-            TileWalker w, wa;
+            TileWalker<kShared> w, wa;
             walker(w);
             walker(wa);
             int v0 = 0, v1 = 0;
@@ -716,7 +806,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             // ------------------------------------------------------------ S = Q K^T issuer
             // S(i) occupies entries 9 i .. 9 i + 8 of the S ring (keys as B, query as A).
             if (rank == 0 && lane == 0 && g0 < g1) {
-                TileWalker w;
+                TileWalker<kShared> w;
                 walker(w);
                 int i = 0;
                 bool ok = true;
@@ -758,14 +848,13 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 // -------------------------------------------------------- O += P V issuer
                 // V(i) occupies the next np entries of the V ring (one per page).
                 if (lane == 0 && g0 < g1) {
-                    TileWalker w;
+                    TileWalker<kShared> w;
                     walker(w);
                     int i = 0, tails = 0, e = 0;
                     bool ok = true;
                     const uint64_t a0 = ptx::smem_desc_sw128(sbase + kOffP, 16, 1024);
                     while (ok && !w.done()) {
                         const Tile t = w.next();
-                        const bool tail = t.unit_end && (t.kv % kPage) != 0;
                         // P is written in two halves: keys [0,128) (pages 0, 1) by the
                         // softmax warps of TMEM lanes 0-63, keys [128,256) by those of
                         // lanes 64-127; each half is released as soon as its pages'
@@ -777,8 +866,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                                 ptx::tc_fence_after();
                             }
                             if (pg >= t.np) continue;
-                            if (tail && pg == t.np - 1) {
-                                // the unit's last page holds rows past the end: once its V
+                            if (tail_page<kShared>(t, pg)) {
+                                // the page holds rows past the end: once its V
                                 // entry has landed, the softmax warps of both CTAs zero those
                                 // rows (entries are consumed in ring order, so the earlier
                                 // pages' slots are already free for this load)
@@ -835,12 +924,15 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         const int st = sw * 32 + lane;               // 0 .. 255 over the softmax warps
         const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(wq * 32) << 16);
         float* xmax = reinterpret_cast<float*>(smem + kOffXmax);   // [cg][l]
-        TileWalker w;
+        TileWalker<kShared> w;
         walker(w);
         int i = 0, tails = 0;
         int v_before = 0;      // V ring entries of tiles before i
         bool ok = true;
         float m_used = -INFINITY, l_part = 0.f;
+        // this thread's row of the unit and the row's token in a unit of several
+        const int unit_row = 64 * static_cast<int>(rank) + m;
+        const int row_tok = kShared ? unit_row / p.um.n_h : 0;
         // the four partial values of row m (both key halves, both column groups)
         auto row_max4 = [&]() {
             return fmaxf(fmaxf(xmax[m], xmax[64 + m]), fmaxf(xmax[128 + m], xmax[192 + m]));
@@ -848,7 +940,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         while (ok && !w.done()) {
             const Tile t = w.next();
             // keys of this tile that belong to this segment
-            const int key_end = min(t.kv, kPage * (t.page0 + t.np));
+            int key_end = min(t.kv, kPage * (t.page0 + t.np));
+            if constexpr (kShared) key_end = min(key_end, t.kv - max(0, t.n_tok - 1 - row_tok));
             if (t.first) {
                 m_used = -INFINITY;
                 l_part = 0.f;
@@ -884,13 +977,15 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 new_m = mx;
                 resc = !t.first;
             }
-            const float alpha = ex2(m_used - new_m);
+            float alpha = ex2(m_used - new_m);
+            // a row of the shared decode may see none of the keys so far
+            if (kShared && new_m == -INFINITY) alpha = 1.f;
             m_used = new_m;
 
             // The weights of row m, keys key0 + [0, 64): computed into registers
             // first, which ends this thread's reads of the S buffer.
             float ps2[2] = {0.f, 0.f};
-            const float neg_m = -m_used;
+            const float neg_m = kShared && m_used == -INFINITY ? 0.f : -m_used;
             uint32_t pk[32];
             {
                 uint32_t r[2][32];
@@ -949,15 +1044,17 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             // V ring position of this tile's entries (one per page)
             const int v_start = v_before;
             v_before += t.np;
-            if (t.unit_end && (t.kv % kPage) != 0) {
-                // zero rows past the end in this CTA's V entry of the last page
+            for (int pg = kShared ? 0 : t.np - 1; pg < t.np; ++pg) {
+                if (!tail_page<kShared>(t, pg)) continue;
+                // zero the rows past the end in this CTA's V entry of the page
                 // (4 chunks of 64 rows x 128 B)
                 ok = wait_bar(bar(BAR_TAIL_READY), tails & 1, abort_flag, p.status, tmo);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ++tails;
-                const int valid = t.kv - kPage * (t.page0 + t.np - 1);
+                const int left = t.kv - kPage * (t.page0 + pg);   // keys from the page's first row on
+                const int valid = kShared ? max(0, min(left, kPage)) : left;
                 const int bad = kPage - valid;
-                const int et = v_start + (t.np - 1);
+                const int et = v_start + pg;
                 unsigned char* ent = smem + kOffVRing + (et % kVRing) * kVEntry;
                 for (int x = st; x < 4 * bad * 8; x += 256) {
                     const int chunk = x / (bad * 8);
@@ -965,10 +1062,27 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                     const int row = valid + (rem >> 3), ch = rem & 7;
                     reinterpret_cast<uint4*>(ent + chunk * kBox + row * 128)[ch] = make_uint4(0, 0, 0, 0);
                 }
+                if constexpr (kShared) {
+                    // Rows that only the unit's later tokens see: a weight of zero
+                    // hides them from the earlier ones, unless they hold infinities
+                    // or NaN, which are dropped here.  The tokens that do see such a
+                    // row have a score, and so an output, that is not finite.
+                    const int from = max(0, left - (t.n_tok - 1)), part = valid - from;
+                    for (int x = st; x < 4 * part * 8; x += 256) {
+                        const int chunk = x / (part * 8);
+                        const int rem = x - chunk * part * 8;
+                        uint4* at = reinterpret_cast<uint4*>(ent + chunk * kBox + (from + (rem >> 3)) * 128) + (rem & 7);
+                        const uint4 v = *at;
+                        const uint4 c = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
+                                                   finite_bf16x2(v.w));
+                        if (c.x != v.x || c.y != v.y || c.z != v.z || c.w != v.w) *at = c;
+                    }
+                }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(BAR_TAIL_DONE));
             }
+            if (kShared && !__all_sync(0xffffffffu, ok)) { ok = false; break; }
 
             if (t.last) {
                 // ---- epilogue of this unit segment: wait for P.V of this tile (all
@@ -982,11 +1096,15 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 ptx::named_bar_sync(2, 256);
                 const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
                 const float lse = lsum > 0.f ? (m_used + __log2f(lsum)) * kLn2 : -INFINITY;
-                const int bt = t.bt, hb = t.hb;
-                const int head_in_unit = 64 * static_cast<int>(rank) + m;
-                const bool whole = t.whole;
-                const size_t grow = static_cast<size_t>(bt) * p.n_h + hb * 128 + head_in_unit;
-                const size_t slot = static_cast<size_t>(cluster) + t.u;
+                const bool whole = t.whole && !(kShared && p.um.n_prefix > 0);
+                const size_t grow = static_cast<size_t>(t.row0) + unit_row;
+                // the first row of the unit's partial slot
+                size_t slot_row = (static_cast<size_t>(cluster) + t.u) * 128;
+                int warp_rows = 32;   // rows of this warp that belong to the unit
+                if constexpr (kShared) {
+                    warp_rows = t.rows - (unit_row - lane);
+                    if (t.u >= p.um.n_prefix) slot_row = own_slot_row(cluster, t.u - p.um.n_prefix, p.um);
+                }
                 // This warp's 32 rows (consecutive heads) x the thread's 128
                 // latent columns go out through 4 KB tiles written in the
                 // 128-byte swizzled layout of a TMA store box (a thread's row of
@@ -1005,12 +1123,26 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 const uint32_t stage_u = sbase + stage_off;
                 const int x7 = lane & 7;
                 const int row0 = whole ? static_cast<int>(grow - lane)
-                                       : static_cast<int>(slot * 128 + head_in_unit - lane);
+                                       : static_cast<int>(slot_row + unit_row - lane);
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < (warp_rows > 0 ? 4 : 0); ++q) {
                     uint32_t o[32];
                     ptx::tmem_ld32(t_lane + kTmemO + 128 * h + 32 * q, o);
                     ptx::tmem_wait_ld();
+                    if (kShared && whole && warp_rows < 32) {
+                        // the store's box would reach into another unit's rows
+                        uint4* dst = reinterpret_cast<uint4*>(p.out_latent + grow * kDc + col0 + 32 * q);
+                        if (lane < warp_rows) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dst[k] = make_uint4(
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 0]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+                        }
+                        continue;
+                    }
                     const int tile_k = whole ? (q >> 1) : q;   // this round's store
                     const uint32_t tile_off = final_tile ? 4096u * tile_k : 0u;
                     unsigned char* my_row = stage + tile_off + lane * 128;
@@ -1055,9 +1187,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                     if (lane == 0) ptx::bulk_wait_read_all();   // the P buffer is written again by the next tile
                     __syncwarp();
                 }
-                if (!hi && cg == 0) {
+                if (!hi && cg == 0 && (!kShared || lane < warp_rows)) {
                     if (whole) p.out_lse[grow] = lse;
-                    else p.part_lse[slot * 128 + head_in_unit] = lse;
+                    else p.part_lse[slot_row + unit_row] = lse;
                 }
                 ptx::tc_fence_before();
             }
@@ -1089,9 +1221,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
 // merge metadata and each cluster's page range, computed by one block of 1024
 // threads with the same cut rule as the decode kernel's own scan.
 // ---------------------------------------------------------------------------
+template <bool kShared>
 __global__ void __launch_bounds__(1024)
-mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, int B, int T_q, int n_hb, int max_blocks,
-                          int max_splits, int U, int32_t* __restrict__ prefix, int32_t* __restrict__ tprefix,
+mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um, int max_splits, int U, int32_t* __restrict__ prefix, int32_t* __restrict__ tprefix,
                           int32_t* __restrict__ wprefix, int32_t* __restrict__ kv_out, int4* __restrict__ unit_meta,
                           int4* __restrict__ cluster_info, int32_t* status) {
     __shared__ int warp_tot[3][32];
@@ -1105,7 +1237,7 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, int B, int T_q, 
         const int u = base + threadIdx.x;
         int v[3] = {0, 0, 0};   // pages, tiles, cost
         if (u < U) {
-            const int kv = unit_keys(seq_lens, u, n_hb, B, T_q, max_blocks);
+            const int kv = unit_keys<kShared>(seq_lens, u, um);
             kv_out[u] = kv;
             v[0] = (kv + kPage - 1) / kPage;
             v[1] = (v[0] + kTilePages - 1) / kTilePages;
@@ -1151,9 +1283,9 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, int B, int T_q, 
     __shared__ int cuts[kClusters + 1], cut_tmp[kClusters + 1];
     compute_cuts(cuts, cut_tmp, prefix, tprefix, wprefix, U, T, Tt, max_splits);
     for (int u = threadIdx.x; u < U; u += 1024) {
-        const int4 m = unit_meta_of(u, prefix, cuts, seq_lens, n_hb, B, T_q, max_blocks);
+        const int4 m = unit_meta_of<kShared>(u, prefix, cuts, seq_lens, um);
         unit_meta[u] = m;
-        if (m.x == 0 && u < B * n_hb && u % n_hb == 0) raise_status(status, MLA_STATUS_BAD_SEQ_LEN);
+        if (m.x == 0 && first_of_sequence<kShared>(u, um)) raise_status(status, MLA_STATUS_BAD_SEQ_LEN);
     }
     for (int c = threadIdx.x; c < kClusters; c += 1024) {
         const int a = cuts[c], e = cuts[c + 1];
@@ -1249,6 +1381,101 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
     if (lane == 0) out_lse[grow] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
+// The same for the shared decode: one warp per query row.  With prefix units
+// the row's partials are those of its prefix unit and of its sequence unit;
+// otherwise only units cut between clusters left partials.
+__global__ void __launch_bounds__(256, 3)
+mla_sm100_merge_shared_kernel(const int4* __restrict__ unit_meta, const float* __restrict__ part_o,
+                              const float* __restrict__ part_lse, uint16_t* __restrict__ out_latent,
+                              float* __restrict__ out_lse, const UnitMap um) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int grow = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (grow >= um.n_rows) return;
+    const int n = grow / um.n_h, head = grow - n * um.n_h;
+    const int b = n / um.T_q, t = n - b * um.T_q;
+    const int group = t / um.tok_per_unit;
+    const int hb = um.tok_per_unit > 1 ? 0 : head >> 7;
+    const int unit_row = um.tok_per_unit > 1 ? (t - group * um.tok_per_unit) * um.n_h + head : head & 127;
+    const int uo = (group * um.B + b) * um.n_hb + hb;
+    const int4 own = unit_meta[um.n_prefix + uo];
+    uint4* dst = reinterpret_cast<uint4*>(out_latent + static_cast<size_t>(grow) * kDc + lane * 16);
+    if (own.x == 0) {   // the sequence's length is out of range
+        dst[0] = make_uint4(0, 0, 0, 0);
+        dst[1] = make_uint4(0, 0, 0, 0);
+        if (lane == 0) out_lse[grow] = -INFINITY;
+        return;
+    }
+    int n_pre = 0;   // partials of the prefix unit
+    size_t pre_row = 0;
+    if (um.n_prefix > 0) {
+        const int4 pre = unit_meta[grow >> 7];
+        n_pre = pre.z;
+        pre_row = (static_cast<size_t>(pre.y) + (grow >> 7)) * 128 + (grow & 127);
+    } else if (own.z <= 1) {
+        return;   // written by the decode kernel
+    }
+    const size_t own_row = own_slot_row(own.y, uo, um) + unit_row;
+    const int parts = n_pre + own.z;   // <= 2 kClusters
+    auto row_of = [&](int i) {
+        return i < n_pre ? pre_row + static_cast<size_t>(i) * 128
+                         : own_row + static_cast<size_t>(i - n_pre) * um.own_rows;
+    };
+    auto load_pair = [&](float4 (&v)[2][4], int i) {   // partials i, i + 1 (zeros past the last)
+        const float4* a = reinterpret_cast<const float4*>(part_o + row_of(i) * kDc) + lane * 4;
+        const float4* c = reinterpret_cast<const float4*>(part_o + row_of(min(i + 1, parts - 1)) * kDc) + lane * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[0][k] = __ldcg(a + k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[1][k] = i + 1 < parts ? __ldcg(c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 v[2][4];
+    load_pair(v, 0);
+    constexpr int kPer = (2 * kClusters + 31) / 32;   // partial lane + 32 k in ls[k]
+    float ls[kPer];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        ls[k] = lane + 32 * k < parts ? __ldcg(part_lse + row_of(lane + 32 * k)) : -INFINITY;
+        mx = fmaxf(mx, ls[k]);
+    }
+    mx = warp_max(mx);
+    auto w_of = [&](float l) { return l == -INFINITY ? 0.f : ex2((l - mx) * kLog2e); };
+    float z = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) z += w_of(ls[k]);
+    z = warp_sum(z);
+    auto weight = [&](int i) {
+        float l = ls[0];
+#pragma unroll
+        for (int k = 1; k < kPer; ++k) l = (i >> 5) == k ? ls[k] : l;
+        return w_of(__shfl_sync(0xffffffffu, l, i & 31));
+    };
+    float acc[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+    for (int i = 0; i < parts; i += 2) {
+        if (i > 0) load_pair(v, i);
+        const float w0 = weight(i), w1 = i + 1 < parts ? weight(i + 1) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // a partial of weight zero holds nothing that the row sees
+            acc[4 * k + 0] += (w0 != 0.f ? w0 * v[0][k].x : 0.f) + (w1 != 0.f ? w1 * v[1][k].x : 0.f);
+            acc[4 * k + 1] += (w0 != 0.f ? w0 * v[0][k].y : 0.f) + (w1 != 0.f ? w1 * v[1][k].y : 0.f);
+            acc[4 * k + 2] += (w0 != 0.f ? w0 * v[0][k].z : 0.f) + (w1 != 0.f ? w1 * v[1][k].z : 0.f);
+            acc[4 * k + 3] += (w0 != 0.f ? w0 * v[0][k].w : 0.f) + (w1 != 0.f ? w1 * v[1][k].w : 0.f);
+        }
+    }
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    uint32_t pk[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    if (lane == 0) out_lse[grow] = z > 0.f ? mx + logf(z) : -INFINITY;
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1269,7 +1496,8 @@ struct Sm100Ws {
     size_t prefix, tprefix, wprefix, kv, kv_cta, meta, cinfo, part_lse, part_o, total;
 };
 
-Sm100Ws sm100_ws(int U) {
+// U units whose partial slots take part_rows rows in all
+Sm100Ws sm100_ws(int U, size_t part_rows) {
     Sm100Ws w;
     w.prefix = 0;
     w.tprefix = w.prefix + r256(static_cast<size_t>(U + 1) * 4);
@@ -1279,9 +1507,50 @@ Sm100Ws sm100_ws(int U) {
     w.meta = w.kv_cta + r256(static_cast<size_t>(2 * kClusters) * U * 4);
     w.cinfo = w.meta + r256(static_cast<size_t>(U) * 16);
     w.part_lse = w.cinfo + r256(static_cast<size_t>(kClusters) * 16);
-    w.part_o = w.part_lse + r256(static_cast<size_t>(kClusters + U) * 128 * 4);
-    w.total = w.part_o + r256(static_cast<size_t>(kClusters + U) * 128 * kDc * 4);
+    w.part_o = w.part_lse + r256(part_rows * 4);
+    w.total = w.part_o + r256(part_rows * kDc * 4);
     return w;
+}
+Sm100Ws sm100_ws(int U) { return sm100_ws(U, static_cast<size_t>(kClusters + U) * 128); }
+
+// The shared decode's units.
+struct SharedPlan {
+    UnitMap um;
+    long U;
+    size_t part_rows;
+};
+
+SharedPlan shared_plan(int n_h, int B, int T_q, int max_blocks, int n_shared, bool prefix_units) {
+    SharedPlan s;
+    s.um.n_h = n_h;
+    s.um.n_hb = (n_h + 127) / 128;
+    s.um.B = B;
+    s.um.T_q = T_q;
+    s.um.max_blocks = max_blocks;
+    s.um.n_shared = n_shared;
+    s.um.n_rows = B * T_q * n_h;
+    int per = n_h > 64 ? 1 : 128 / n_h;
+    per = per < 64 ? per : 64;
+    s.um.tok_per_unit = per < T_q ? per : T_q;
+    const int rows = s.um.tok_per_unit > 1 ? s.um.tok_per_unit * n_h : (n_h < 128 ? n_h : 128);
+    s.um.own_rows = (rows + 31) / 32 * 32;
+    s.um.n_prefix = prefix_units ? (s.um.n_rows + 127) / 128 : 0;
+    const long own = static_cast<long>(B) * ((T_q + s.um.tok_per_unit - 1) / s.um.tok_per_unit) * s.um.n_hb;
+    s.U = s.um.n_prefix + own;
+    s.part_rows = static_cast<size_t>(kClusters + own) * s.um.own_rows +
+                  (prefix_units ? static_cast<size_t>(kClusters + s.um.n_prefix) * 128 : 0);
+    return s;
+}
+
+// Whether the shared pages get units of their own: where the sequences' units
+// leave so many of their 128 rows empty that walking the shared pages in each
+// of them costs more tiles than the extra units' epilogues and the merge of
+// every row.
+bool use_prefix_units(int n_h, int B, int T_q, int n_shared) {
+    if (n_shared == 0) return false;
+    const SharedPlan s = shared_plan(n_h, B, T_q, n_shared, n_shared, true);
+    const long own = s.U - s.um.n_prefix;
+    return (own - s.um.n_prefix) * ((n_shared + kTilePages - 1) / kTilePages) > s.um.n_prefix + own;
 }
 
 // Test hook state: the next launch withholds one load and uses this wait bound.
@@ -1307,11 +1576,17 @@ size_t sm100_unit_meta_offset(int n_h, int B, int T_q) { return sm100_ws(B * T_q
 
 void sm100_arm_timeout_test(uint64_t wait_limit_ns) { g_test_wait_limit_ns.store(wait_limit_ns); }
 
-cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits, cudaStream_t stream) {
-    const int n_hb = P.n_h / 128;
-    const int U = P.B * P.T_q * n_hb;
-    if (U > 65535) return cudaErrorInvalidValue;
-    const Sm100Ws w = sm100_ws(U);
+size_t sm100_shared_workspace_bytes(int n_h, int B, int T_q) {
+    const SharedPlan s = shared_plan(n_h, B, T_q, 1, 1, true);
+    return sm100_ws(static_cast<int>(s.U), s.part_rows).total;
+}
+
+namespace {
+
+template <bool kShared>
+cudaError_t launch_units(const DecodeParams& P, const UnitMap& um, int U, size_t part_rows, void* ws, int max_splits,
+                         cudaStream_t stream) {
+    const Sm100Ws w = sm100_ws(U, part_rows);
     char* base = static_cast<char*>(ws);
     Sm100Params k;
     const uint64_t pool_rows = static_cast<uint64_t>(P.num_blocks) * P.block_size;
@@ -1321,10 +1596,10 @@ cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits,
         !make_map_2d(&k.tm_qa, P.q_abs, kDc, q_rows, kDc * 2, 64, 64) ||
         !make_map_2d(&k.tm_qr, P.q_r, kDr, q_rows, kDr * 2, 64, 64) ||
         !make_map_2d(&k.tm_out, P.out_latent, kDc, q_rows, kDc * 2, 64, 32) ||
-        !make_map_2d_f32(&k.tm_part, base + w.part_o, kDc, static_cast<uint64_t>(kClusters + U) * 128, kDc * 4, 32,
-                         32))
+        !make_map_2d_f32(&k.tm_part, base + w.part_o, kDc, part_rows, kDc * 4, 32, 32))
         return cudaErrorInvalidValue;
     k.block_table = P.block_table;
+    k.shared_table = P.shared_table;
     k.seq_lens = P.seq_lens;
     k.prefix = reinterpret_cast<int32_t*>(base + w.prefix);
     k.unit_kv = reinterpret_cast<int32_t*>(base + w.kv);
@@ -1336,13 +1611,9 @@ cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits,
     k.part_o = reinterpret_cast<float*>(base + w.part_o);
     k.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     k.status = P.status;
-    k.n_h = P.n_h;
-    k.n_hb = n_hb;
-    k.B = P.B;
-    k.T_q = P.T_q;
+    k.um = um;
     k.U = U;
     k.num_blocks = P.num_blocks;
-    k.max_blocks = P.max_blocks;
     k.max_splits = max_splits;
     k.in_kernel_schedule = U <= kInKernelUnits ? 1 : 0;
     const uint64_t test_limit = g_test_wait_limit_ns.exchange(0);
@@ -1352,22 +1623,45 @@ cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits,
 
     cudaError_t e;
     if (!k.in_kernel_schedule) {
-        e = launch_pdl(mla_sm100_schedule_kernel, dim3(1), dim3(1024), 0, stream, P.seq_lens, P.B, P.T_q, n_hb,
-                       P.max_blocks, max_splits, U, k.prefix, reinterpret_cast<int32_t*>(base + w.tprefix),
-                       reinterpret_cast<int32_t*>(base + w.wprefix),
-                       k.unit_kv, k.unit_meta,
+        e = launch_pdl(mla_sm100_schedule_kernel<kShared>, dim3(1), dim3(1024), 0, stream, P.seq_lens, um, max_splits,
+                       U, k.prefix, reinterpret_cast<int32_t*>(base + w.tprefix),
+                       reinterpret_cast<int32_t*>(base + w.wprefix), k.unit_kv, k.unit_meta,
                        reinterpret_cast<int4*>(base + w.cinfo), P.status);
         if (e != cudaSuccess) return e;
     }
     static std::atomic<uint64_t> smem_set{0};
-    e = allow_smem_once(mla_decode_sm100_kernel, static_cast<int>(kSmemBytes), smem_set);
+    e = allow_smem_once(mla_decode_sm100_kernel<kShared>, static_cast<int>(kSmemBytes), smem_set);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(mla_decode_sm100_kernel, dim3(2 * kClusters), dim3(kThreads), kSmemBytes, stream, k);
+    e = launch_pdl(mla_decode_sm100_kernel<kShared>, dim3(2 * kClusters), dim3(kThreads), kSmemBytes, stream, k);
     if (e != cudaSuccess) return e;
+    if constexpr (kShared)
+        return launch_pdl(mla_sm100_merge_shared_kernel, dim3((um.n_rows + 7) / 8), dim3(256), 0, stream,
+                          static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),
+                          static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, um);
     const int rows = U * 128;
     return launch_pdl(mla_sm100_merge_kernel, dim3((rows + 7) / 8), dim3(256), 0, stream,
                       static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),
-                      static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, P.n_h, n_hb, P.B, P.T_q, U);
+                      static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, P.n_h, um.n_hb, P.B, P.T_q, U);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits, cudaStream_t stream) {
+    UnitMap um = {};
+    um.n_h = P.n_h;
+    um.n_hb = P.n_h / 128;
+    um.B = P.B;
+    um.T_q = P.T_q;
+    um.max_blocks = P.max_blocks;
+    const int U = P.B * P.T_q * um.n_hb;
+    if (U > 65535) return cudaErrorInvalidValue;
+    return launch_units<false>(P, um, U, static_cast<size_t>(kClusters + U) * 128, ws, max_splits, stream);
+}
+
+cudaError_t launch_decode_shared_sm100(const DecodeParams& P, void* ws, int max_splits, cudaStream_t stream) {
+    const SharedPlan s = shared_plan(P.n_h, P.B, P.T_q, P.max_blocks, P.n_shared,
+                                     use_prefix_units(P.n_h, P.B, P.T_q, P.n_shared));
+    return launch_units<true>(P, s.um, static_cast<int>(s.U), s.part_rows, ws, max_splits, stream);
 }
 
 }  // namespace mla

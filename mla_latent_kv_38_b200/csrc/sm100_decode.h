@@ -21,4 +21,9 @@ size_t sm100_unit_meta_offset(int n_h, int B, int T_q);
 void sm100_arm_timeout_test(uint64_t wait_limit_ns);
 cudaError_t launch_decode_sm100(const DecodeParams& P, void* ws, int max_splits, cudaStream_t stream);
 
+// The decode of a batch behind P.n_shared shared pages (any n_h).  The caller
+// keeps B T_q ceil(n_h / 128) max_blocks below 2^29.
+size_t sm100_shared_workspace_bytes(int n_h, int B, int T_q);
+cudaError_t launch_decode_shared_sm100(const DecodeParams& P, void* ws, int max_splits, cudaStream_t stream);
+
 }  // namespace mla
