@@ -1,50 +1,455 @@
 // Projection in 8-bit integers with a scale per token and per output channel:
 //   out[n][o] = (sum_k x8[n][k] w8[o][k]) x_scale[n] w_scale[o]
-// (the integer sum is exact: |sum| <= 65,536 x 128^2 = 2^30).
+// on tcgen05 (kind::i8, 32-bit integer accumulators).  |sum| <= 65,536 x 128^2
+// = 2^30, so the sum is exact, in any order.  Both operands are K-major bytes,
+// read by TMA in chunks of 128 columns (128-byte swizzle); columns past d_in,
+// rows past n_tok and d_out read as zero.
+//
+// Two kernels, chosen by use_wide():
+//  * split: few tokens.  Bound by the weights' bytes.  A CTA takes 128 channels
+//    (MMA M) against up to 256 tokens (MMA N); the K axis is cut over the CTAs
+//    of a cluster, so that every SM streams weights even where there are fewer
+//    channel tiles than SMs, and the partial sums meet in distributed shared
+//    memory: no workspace, no second launch.
+//  * wide: many tokens.  Bound by the tensor cores.  Persistent clusters of two
+//    CTAs issue cta_group::2 MMAs of 256 tokens x 256 channels (each SM supplies
+//    half of each operand); two accumulators in tensor memory let the epilogue
+//    of one tile run under the MMAs of the next.
+
+#include <cuda.h>
 
 #include "common.cuh"
 #include "layer.h"
+#include "sm100_ptx.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
 
-// 64 tokens x 64 channels per block, 4 x 4 per thread, K in steps of 64 bytes
-// through shared memory, four products an instruction (dp4a).
-__global__ void __launch_bounds__(256) linear_i8_kernel(const int8_t* __restrict__ x8, long ld_x,
-                                                        const float* __restrict__ x_scale,
-                                                        const int8_t* __restrict__ w8,
-                                                        const float* __restrict__ w_scale, uint16_t* __restrict__ out,
-                                                        int n_tok, int d_in, int d_out) {
-    __shared__ int xs[16][64 + 1], ws[16][64 + 1];
-    griddep_launch_dependents();
-    griddep_wait();
-    const long n0 = blockIdx.y * 64L, o0 = blockIdx.x * 64L;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < d_in; k0 += 64) {
-        for (int e = threadIdx.x; e < 1024; e += 256) {
-            const int r = e >> 4, k = e & 15;
-            const bool in = k0 + 4 * k < d_in;
-            xs[k][r] = in && n0 + r < n_tok ? *reinterpret_cast<const int*>(x8 + (n0 + r) * ld_x + k0 + 4 * k) : 0;
-            ws[k][r] = in && o0 + r < d_out ? *reinterpret_cast<const int*>(w8 + (o0 + r) * d_in + k0 + 4 * k) : 0;
+constexpr uint64_t kTimeoutNs = 2000000000ull;   // bound of every wait
+constexpr int kSms = 148;
+constexpr uint32_t kChunk = 128;                 // columns (bytes) of one K chunk
+constexpr uint32_t kOpBytes = 128 * kChunk;      // a chunk of 128 operand rows (16 KB)
+
+// An int8 matrix, rows row_bytes apart, in boxes of 128 columns x box_rows.
+bool make_map_i8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
+                 uint32_t box_rows) {
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {kChunk, box_rows};
+    return encode_tiled_cached(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             int32_t* status) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait_suspend(bar, parity, 100000)) {
+        if (*abort_flag) return false;
+        if (ptx::global_timer_ns() - t0 > kTimeoutNs) {
+            *abort_flag = 1;
+            raise_status(status, MLA_STATUS_TIMEOUT);
+            return false;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xs[k][ty + 16 * i], ws[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long n = n0 + ty + 16 * i, o = o0 + tx + 16 * j;
-            if (n < n_tok && o < d_out)
-                out[n * d_out + o] = f2bf(static_cast<float>(acc[i][j]) * x_scale[n] * w_scale[o]);
+    return true;
+}
+
+// after an abort: copies still in flight get time to land before shared memory is released
+__device__ __forceinline__ void settle_copies(volatile int* abort_flag) {
+    if (!*abort_flag) return;
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (ptx::global_timer_ns() - t0 < 200000ull) {
+    }
+}
+
+__device__ __forceinline__ float scaled(int sum, float sx, float sw) { return static_cast<float>(sum) * sx * sw; }
+
+// ---------------------------------------------------------------------------
+// split
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitThreads = 128;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kSplitRing = 200 * 1024;       // one CTA per SM
+constexpr uint32_t kSplitRingHalf = 108 * 1024;   // two
+
+struct SplitArgs {
+    CUtensorMap tm_w;   // w8 [d_out][d_in], boxes 128 x 128
+    CUtensorMap tm_x;   // x8 [n_tok][d_in], boxes 128 x nt
+    const float* x_scale;
+    const float* w_scale;
+    uint16_t* out;
+    int32_t* status;
+    int n_tok, d_out, nt, chunks, stages;
+    uint32_t idesc, tmem_cols, ring_bytes;
+};
+
+__global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __grid_constant__ SplitArgs p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                           ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int S = p.stages;
+    const uint32_t stage_bytes = kOpBytes + static_cast<uint32_t>(p.nt) * kChunk;
+    const uint32_t bars = sbase + p.ring_bytes;
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (S + s); };
+    const uint32_t done = bars + 8 * (2 * S);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + p.ring_bytes + 8 * (2 * S + 1));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.ring_bytes + 8 * (2 * S + 1) + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = static_cast<int>(ptx::cluster_size()), rank = static_cast<int>(ptx::cluster_rank());
+    const int o0 = static_cast<int>(blockIdx.x) / parts * 128, n0 = blockIdx.y * p.nt;
+    const int c0 = static_cast<int>(static_cast<long>(p.chunks) * rank / parts);
+    const int c1 = static_cast<int>(static_cast<long>(p.chunks) * (rank + 1) / parts);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
         }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    // The weights' first chunks on their way into L2 while the kernel before
+    // this one still runs (a prefetch changes no data, and L2 is coherent with
+    // that kernel's writes, so it may precede the wait).
+    if (warp == 0) {
+        if (lane == 0) {
+            ptx::prefetch_tmap(&p.tm_w);
+            ptx::prefetch_tmap(&p.tm_x);
+        }
+        if (c0 + lane < c1 && lane < S)
+            ptx::tma_prefetch_2d(&p.tm_w, static_cast<int>(kChunk) * (c0 + lane), o0);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc1(ptx::smem_u32(tmem_slot), p.tmem_cols);
+        ptx::tmem_relinquish1();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();   // the codes come from earlier kernels; the output may still be read by them
+
+    if (warp == 0) {
+        // chunk c into stage c mod S; a thread's copies run one after another,
+        // so consecutive stages come from different threads
+        for (int c = 0; c < c1 - c0; ++c) {
+            const int s = c % S;
+            bool ok = true;
+            if (lane == (c & 7)) {
+                ok = wait_bounded(empty(s), ((c / S) & 1) ^ 1, abort_flag, p.status);
+                if (ok) {
+                    const uint32_t st = sbase + s * stage_bytes;
+                    const int k = static_cast<int>(kChunk) * (c0 + c);
+                    ptx::mbar_arrive_expect_tx(full(s), stage_bytes);
+                    ptx::tma_load_2d(st, &p.tm_w, k, o0, full(s));
+                    ptx::tma_load_2d(st + kOpBytes, &p.tm_x, k, n0, full(s));
+                }
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+        }
+    } else if (warp == 1 && lane == 0) {
+        bool ok = true;
+        for (int c = 0; c < c1 - c0 && ok; ++c) {
+            const int s = c % S;
+            ok = wait_bounded(full(s), (c / S) & 1, abort_flag, p.status);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t st = sbase + s * stage_bytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                ptx::mma1_i8_ss(tmem, ptx::smem_desc_sw128(st + kk * 32, 16, 1024),
+                                ptx::smem_desc_sw128(st + kOpBytes + kk * 32, 16, 1024), p.idesc, (c | kk) ? 1u : 0u);
+            ptx::mma1_commit(empty(s));
+        }
+        ptx::mma1_commit(done);   // completes when every MMA issued above has (also on the abort path)
+    }
+    __syncwarp();
+    wait_bounded(done, 0, abort_flag, p.status);
+    settle_copies(abort_flag);
+    __syncthreads();   // every copy into the ring has landed and been read
+    griddep_launch_dependents();
+
+    // Partial sums to shared memory as [token][128 channels] (a warp writes 32
+    // consecutive channels), then the cluster's CTAs share the outputs: each
+    // adds its vectors of four channels over all parts.
+    int* part = reinterpret_cast<int*>(smem);
+    const int valid = min(p.nt, p.n_tok - n0);
+    ptx::tc_fence_after();
+    for (int j0 = 0; j0 < valid; j0 += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + j0, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(j0 + j) * 128 + threadIdx.x] = static_cast<int>(r[j]);
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    for (int e = rank * kSplitThreads + threadIdx.x; e < valid * 32; e += parts * kSplitThreads) {
+        const int j = e >> 5, o = o0 + 4 * (e & 31);
+        if (o >= p.d_out) continue;
+        int4 sum = make_int4(0, 0, 0, 0);
+        for (int q = 0; q < parts; ++q) {
+            const int4 v = ptx::ld_cluster_int4(ptx::map_to_rank(sbase + 16u * static_cast<uint32_t>(e), q));
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const float sx = p.x_scale[n0 + j];
+        const float* sw = p.w_scale + o;
+        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(n0 + j) * p.d_out + o) =
+            make_uint2(pack_bf16x2(scaled(sum.x, sx, sw[0]), scaled(sum.y, sx, sw[1])),
+                       pack_bf16x2(scaled(sum.z, sx, sw[2]), scaled(sum.w, sx, sw[3])));
+    }
+    ptx::cluster_sync();   // the other CTAs have read this one's sums
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc1(tmem, p.tmem_cols);
+}
+
+// ---------------------------------------------------------------------------
+// wide
+// ---------------------------------------------------------------------------
+
+constexpr int kWideThreads = 192;                // loads, MMAs, 4 x epilogue
+constexpr int kWideStages = 6;
+constexpr uint32_t kWideStage = 2 * kOpBytes;    // this CTA's 128 tokens and 128 channels
+constexpr uint32_t kOffStage = kWideStages * kWideStage;       // epilogue staging: 2 x 4 KB per warp
+constexpr uint32_t kOffScales = kOffStage + 4 * 2 * 4096;      // the tile's 256 channel scales
+constexpr uint32_t kOffWideBars = kOffScales + 1024;
+enum { W_FULL = 0, W_EMPTY = W_FULL + kWideStages, W_ACC_FULL = W_EMPTY + kWideStages, W_ACC_FREE = W_ACC_FULL + 2,
+       W_DRAIN = W_ACC_FREE + 2, W_BARS = W_DRAIN + 1 };
+constexpr uint32_t kWideSmem = kOffWideBars + 8 * W_BARS + 16 + 1024;
+static_assert(kWideSmem <= 232448, "shared memory budget");
+
+struct WideArgs {
+    CUtensorMap tm_x;     // x8 [n_tok][d_in], boxes 128 x 128
+    CUtensorMap tm_w;     // w8 [d_out][d_in], boxes 128 x 128
+    CUtensorMap tm_out;   // out [n_tok][d_out] bf16, boxes 64 x 32 (stores)
+    const float* x_scale;
+    const float* w_scale;
+    int32_t* status;
+    int n_tok, d_out, chunks, m_tiles, tiles;
+};
+
+constexpr uint32_t kWideIdesc = ptx::idesc_i8_s32(256, 256);
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                           ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    auto bar = [&](int i) { return sbase + kOffWideBars + 8u * static_cast<uint32_t>(i); };
+    auto leader_bar = [&](int i) { return ptx::map_to_rank(bar(i), 0); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffWideBars + 8 * W_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffWideBars + 8 * W_BARS + 4);
+    const int rank = static_cast<int>(ptx::cluster_rank());
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWideStages; ++s) {
+            ptx::mbar_init(bar(W_FULL + s), 1);     // leader: both CTAs' bytes
+            ptx::mbar_init(bar(W_EMPTY + s), 1);    // each CTA: MMA commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar(W_ACC_FULL + b), 1);   // each CTA: MMA commit
+            ptx::mbar_init(bar(W_ACC_FREE + b), 8);   // leader: 4 epilogue warps x 2 CTAs
+        }
+        ptx::mbar_init(bar(W_DRAIN), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&p.tm_x);
+        ptx::prefetch_tmap(&p.tm_w);
+        ptx::prefetch_tmap(&p.tm_out);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    if (warp == 0) {
+        // tiles in order of channels, all token tiles of a channel tile in a
+        // row: the clusters work on the same weights at the same time
+        int e = 0;
+        bool ok = true;
+        for (int t = cluster; t < p.tiles && ok; t += clusters) {
+            const int n0 = (t % p.m_tiles) * 256 + 128 * rank, o0 = (t / p.m_tiles) * 256 + 128 * rank;
+            for (int c = 0; c < p.chunks; ++c, ++e) {
+                const int s = e % kWideStages;
+                bool good = true;
+                if (lane == s) {
+                    good = wait_bounded(bar(W_EMPTY + s), ((e / kWideStages) & 1) ^ 1, abort_flag, p.status);
+                    if (good) {
+                        const uint32_t st = sbase + s * kWideStage;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(W_FULL + s), 2 * kWideStage);
+                        ptx::tma_load_2d_pair_normal(st, &p.tm_x, static_cast<int>(kChunk) * c, n0, leader_bar(W_FULL + s));
+                        ptx::tma_load_2d_pair_normal(st + kOpBytes, &p.tm_w, static_cast<int>(kChunk) * c, o0,
+                                                     leader_bar(W_FULL + s));
+                    }
+                }
+                if (!__all_sync(0xffffffffu, good)) { ok = false; break; }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int e = 0, i = 0;
+            bool ok = true;
+            for (int t = cluster; t < p.tiles && ok; t += clusters, ++i) {
+                const int b = i & 1;
+                if (!(ok = wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status))) break;
+                ptx::tc_fence_after();
+                for (int c = 0; c < p.chunks; ++c, ++e) {
+                    const int s = e % kWideStages;
+                    if (!(ok = wait_bounded(bar(W_FULL + s), (e / kWideStages) & 1, abort_flag, p.status))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t st = sbase + s * kWideStage;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_pair_i8_ss(tmem + 256 * b, ptx::smem_desc_sw128(st + kk * 32, 16, 1024),
+                                            ptx::smem_desc_sw128(st + kOpBytes + kk * 32, 16, 1024), kWideIdesc,
+                                            (c | kk) ? 1u : 0u);
+                    ptx::mma_commit_pair(bar(W_EMPTY + s), 0x3);
+                }
+                if (ok) ptx::mma_commit_pair(bar(W_ACC_FULL + b), 0x3);
+            }
+            if (!ok) {
+                // let every MMA this thread issued finish before the teardown frees anything
+                ptx::mma_commit_pair(bar(W_DRAIN), 0x1);
+                const uint64_t t0 = ptx::global_timer_ns();
+                while (!ptx::mbar_try_wait(bar(W_DRAIN), 0) && ptx::global_timer_ns() - t0 < kTimeoutNs) {
+                }
+            }
+        }
+    } else {
+        const int wq = warp & 3;   // tensor-memory lane quadrant
+        const int st = (warp - 2) * 32 + lane;
+        float* scales = reinterpret_cast<float*>(smem + kOffScales);
+        unsigned char* stage = smem + kOffStage + (warp - 2) * 8192;
+        const uint32_t stage_u = sbase + kOffStage + (warp - 2) * 8192;
+        const int x7 = lane & 7;
+        int i = 0, stores = 0;
+        for (int t = cluster; t < p.tiles; t += clusters, ++i) {
+            const int row0 = (t % p.m_tiles) * 256 + 128 * rank + 32 * wq, o0 = (t / p.m_tiles) * 256;
+            const int b = i & 1;
+            ptx::named_bar_sync(1, 128);   // every warp has read the last tile's scales
+            for (int k = st; k < 256; k += 128) scales[k] = o0 + k < p.d_out ? p.w_scale[o0 + k] : 0.f;
+            const float sx = row0 + lane < p.n_tok ? p.x_scale[row0 + lane] : 0.f;
+            ptx::named_bar_sync(2, 128);
+            bool ok = wait_bounded(bar(W_ACC_FULL + b), (i >> 1) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                if (!ok || row0 >= p.n_tok || o0 + 64 * q >= p.d_out) break;   // the same for the whole warp
+                uint32_t r[2][32];
+                const uint32_t src = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 256 * b + 64 * q;
+                ptx::tmem_ld32(src, r[0]);
+                ptx::tmem_ld32(src + 32, r[1]);
+                ptx::tmem_wait_ld();
+                // 32 rows x 64 bf16 in the store box's swizzled layout; two
+                // boxes per warp, so one store is read while the next is written
+                if (lane == 0) ptx::bulk_wait_read_but1();
+                __syncwarp();
+                unsigned char* my_row = stage + (stores & 1) * 4096 + lane * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float4 w0 = *reinterpret_cast<const float4*>(scales + 64 * q + 8 * k);
+                    const float4 w1 = *reinterpret_cast<const float4*>(scales + 64 * q + 8 * k + 4);
+                    auto v = [&](int j) { return static_cast<int>(r[k >> 2][(8 * k + j) & 31]); };
+                    *reinterpret_cast<uint4*>(my_row + ((k ^ x7) * 16)) =
+                        make_uint4(pack_bf16x2(scaled(v(0), sx, w0.x), scaled(v(1), sx, w0.y)),
+                                   pack_bf16x2(scaled(v(2), sx, w0.z), scaled(v(3), sx, w0.w)),
+                                   pack_bf16x2(scaled(v(4), sx, w1.x), scaled(v(5), sx, w1.y)),
+                                   pack_bf16x2(scaled(v(6), sx, w1.z), scaled(v(7), sx, w1.w)));
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(&p.tm_out, stage_u + (stores & 1) * 4096, o0 + 64 * q, row0);
+                    ptx::bulk_commit_group();
+                }
+                ++stores;
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+        }
+        if (lane == 0) ptx::bulk_wait_all();
+    }
+    settle_copies(abort_flag);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+    griddep_launch_dependents();
+}
+
+// Many tokens: enough 256 x 256 tiles to fill most of the 74 clusters.
+bool use_wide(int n_tok, int d_out) {
+    const long tiles = static_cast<long>((n_tok + 255) / 256) * ((d_out + 255) / 256);
+    return n_tok > 128 && tiles >= 60;
+}
+
+cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
+                         uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
+    SplitArgs p;
+    const int tok_tiles = (n_tok + 255) / 256, o_tiles = (d_out + 127) / 128;
+    p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
+    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    // the largest cluster that keeps all CTAs resident and gives each two chunks
+    const bool two = p.nt <= 64;   // two CTAs per SM
+    int parts = kMaxCluster;
+    while (parts > 1 && (static_cast<long>(o_tiles) * tok_tiles * parts > (two ? 2 : 1) * kSms || 2 * parts > p.chunks))
+        --parts;
+    const uint32_t stage = kOpBytes + static_cast<uint32_t>(p.nt) * kChunk;
+    const int most = (p.chunks + parts - 1) / parts;   // chunks of one CTA
+    p.stages = static_cast<int>((two ? kSplitRingHalf : kSplitRing) / stage);
+    if (p.stages > most) p.stages = most;
+    p.ring_bytes = p.stages * stage;
+    if (p.ring_bytes < static_cast<uint32_t>(p.nt) * 512) p.ring_bytes = static_cast<uint32_t>(p.nt) * 512;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < static_cast<uint32_t>(p.nt)) p.tmem_cols *= 2;
+    p.idesc = ptx::idesc_i8_s32(128, p.nt);
+    p.x_scale = x_scale, p.w_scale = w_scale, p.out = out, p.status = status;
+    p.n_tok = n_tok, p.d_out = d_out;
+    if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) || !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, p.nt))
+        return cudaErrorInvalidValue;
+    const size_t smem = p.ring_bytes + 8 * (2 * p.stages + 1) + 16 + 1024;
+    static std::atomic<uint64_t> smem_set{0};
+    const cudaError_t e = allow_smem_once(linear_i8_split_kernel, static_cast<int>(kSplitRing + 2048), smem_set);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(linear_i8_split_kernel, dim3(o_tiles * parts, tok_tiles), dim3(kSplitThreads), parts, smem,
+                              stream, p);
+}
+
+cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
+                        uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
+    WideArgs p;
+    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    p.m_tiles = (n_tok + 255) / 256;
+    p.tiles = p.m_tiles * ((d_out + 255) / 256);
+    p.x_scale = x_scale, p.w_scale = w_scale, p.status = status;
+    p.n_tok = n_tok, p.d_out = d_out;
+    if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) || !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, 128) ||
+        !make_map_2d(&p.tm_out, out, d_out, n_tok, static_cast<uint64_t>(d_out) * 2, 64, 32))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> smem_set{0};
+    const cudaError_t e = allow_smem_once(linear_i8_wide_kernel, static_cast<int>(kWideSmem), smem_set);
+    if (e != cudaSuccess) return e;
+    const int clusters = p.tiles < kSms / 2 ? p.tiles : kSms / 2;
+    return launch_pdl(linear_i8_wide_kernel, dim3(2 * clusters), dim3(kWideThreads), kWideSmem, stream, p);
 }
 
 }  // namespace
@@ -52,10 +457,8 @@ __global__ void __launch_bounds__(256) linear_i8_kernel(const int8_t* __restrict
 cudaError_t launch_linear_i8(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8,
                              const float* w_scale, uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status,
                              cudaStream_t stream) {
-    (void)status;
-    const dim3 grid((d_out + 63) / 64, (n_tok + 63) / 64);
-    return launch_pdl(linear_i8_kernel, grid, dim3(256), 0, stream, x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in,
-                      d_out);
+    return (use_wide(n_tok, d_out) ? launch_wide : launch_split)(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out,
+                                                                 status, stream);
 }
 
 }  // namespace mla
