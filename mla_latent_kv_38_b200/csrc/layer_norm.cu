@@ -51,9 +51,19 @@ __device__ __forceinline__ float2 row_reduce(float s, float m, float2 (*red)[32]
     return make_float2(warp_sum(v.x), warp_max(v.y));
 }
 
+// The row's operands that a thread holds, as they lie in memory.
+template <int V>
+struct NormRow {
+    uint4 u[V], gate[V], res[V];
+};
+
 // V vectors of 8 values per thread; kWarpRow: a row per warp, else per block.
-template <int V, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) block_norm_kernel(const BlockNormArgs a) {
+// All of a row's operands are requested together, in front of the first
+// reduction, and kAhead requests the block's next row there too: with the
+// loads behind the reductions the kernel ran at a third of the memory rate.
+template <int V, bool kWarpRow, bool kAhead>
+__global__ void __launch_bounds__(kWarpRow ? 256 : (V <= 2 ? 640 : 512), kWarpRow ? 4 - V : 1)
+block_norm_kernel(const BlockNormArgs a) {
     __shared__ float2 red[2][32];
     griddep_launch_dependents();
     griddep_wait();
@@ -62,46 +72,56 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) block_norm_kernel(const
     const int T = kWarpRow ? 32 : blockDim.x;
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
     const int per = kWarpRow ? blockDim.x >> 5 : 1;
-    const long row0 = static_cast<long>(blockIdx.x) * per + (kWarpRow ? threadIdx.x >> 5 : 0);
+    const long step = static_cast<long>(gridDim.x) * per;
     const float inv_d = 1.f / static_cast<float>(a.d);
-    for (long row = row0; row < a.n_tok; row += static_cast<long>(gridDim.x) * per) {
+    auto fetch = [&](NormRow<V>& r, long row) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int j = t + k * T;
+            const bool in = j < nv;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            r.u[k] = in ? reinterpret_cast<const uint4*>(a.u + row * a.ld_u)[j] : zero;
+            if (a.gate != nullptr) r.gate[k] = in ? reinterpret_cast<const uint4*>(a.gate + row * a.ld_gate)[j] : zero;
+            if (a.residual != nullptr)
+                r.res[k] = in ? reinterpret_cast<const uint4*>(a.residual + row * a.d)[j] : zero;
+        }
+    };
+    long row = static_cast<long>(blockIdx.x) * per + (kWarpRow ? threadIdx.x >> 5 : 0);
+    NormRow<V> cur, next;
+    if (row < a.n_tok) fetch(cur, row);
+    for (; row < a.n_tok; row += step) {
+        if (kAhead && row + step < a.n_tok) fetch(next, row + step);
         float x[V][8];
+        float rstd = 1.f;
+        if (a.w_post != nullptr) {
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                unpack8(cur.u[k], x[k]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
+            }
+            rstd = rsqrtf(row_reduce<kWarpRow>(s, 0.f, red, turn).x * inv_d + a.eps);
+        }
         float s = 0.f, m = 0.f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int j = t + k * T;
-            if (j < nv) {
-                unpack8(reinterpret_cast<const uint4*>(a.u + row * a.ld_u)[j], x[k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
-        }
-        float rstd = 1.f;
-        if (a.w_post != nullptr) rstd = rsqrtf(row_reduce<kWarpRow>(s, 0.f, red, turn).x * inv_d + a.eps);
-        s = 0.f;
-        float y[V][8];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int j = t + k * T;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[k][e] = 0.f;
             if (j >= nv) continue;
             float f[8];
+            unpack8(cur.u[k], x[k]);
             if (a.w_post != nullptr) {
                 unpack8(reinterpret_cast<const uint4*>(a.w_post)[j], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * rstd * f[e];
             }
             if (a.gate != nullptr) {
-                unpack8(reinterpret_cast<const uint4*>(a.gate + row * a.ld_gate)[j], f);
+                unpack8(cur.gate[k], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[k][e] *= f[e];
             }
             if (a.residual != nullptr) {
-                unpack8(reinterpret_cast<const uint4*>(a.residual + row * a.d)[j], f);
+                unpack8(cur.res[k], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[k][e] = fmaf(a.alpha, x[k][e], f[e]);
             }
@@ -112,33 +132,36 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) block_norm_kernel(const
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     s = fmaf(x[k][e], x[k][e], s);
-                    y[k][e] = x[k][e] * f[e];
-                    m = fmaxf(m, fabsf(y[k][e]));
+                    x[k][e] *= f[e];
+                    m = fmaxf(m, fabsf(x[k][e]));
                 }
             }
         }
-        if (a.w_pre == nullptr) continue;
-        const float2 tot = row_reduce<kWarpRow>(s, m, red, turn);
-        rstd = rsqrtf(tot.x * inv_d + a.eps);
-        // the norm's factor is common to the row: the codes follow from r w_pre alone
-        const float inv = tot.y > 0.f ? __fdiv_rn(127.f, tot.y) : 0.f;
+        if (a.w_pre != nullptr) {
+            const float2 tot = row_reduce<kWarpRow>(s, m, red, turn);
+            rstd = rsqrtf(tot.x * inv_d + a.eps);
+            // the norm's factor is common to the row: the codes follow from r w_pre alone
+            const float inv = tot.y > 0.f ? __fdiv_rn(127.f, tot.y) : 0.f;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int j = t + k * T;
-            if (j >= nv) continue;
-            if (a.out8 != nullptr) {
+            for (int k = 0; k < V; ++k) {
+                const int j = t + k * T;
+                if (j >= nv) continue;
                 float c[8];
+                if (a.out8 != nullptr) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) c[e] = y[k][e] * inv;
-                reinterpret_cast<uint2*>(a.out8 + row * a.d)[j] = pack_codes(c);
-            }
-            if (a.out != nullptr) {
+                    for (int e = 0; e < 8; ++e) c[e] = x[k][e] * inv;
+                    reinterpret_cast<uint2*>(a.out8 + row * a.d)[j] = pack_codes(c);
+                }
+                if (a.out != nullptr) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[k][e] *= rstd;
-                reinterpret_cast<uint4*>(a.out + row * a.d)[j] = pack8(y[k]);
+                    for (int e = 0; e < 8; ++e) c[e] = x[k][e] * rstd;
+                    reinterpret_cast<uint4*>(a.out + row * a.d)[j] = pack8(c);
+                }
             }
+            if (a.out8 != nullptr && t == 0) a.out8_scale[row] = __fdiv_rn(tot.y * rstd, 127.f);
         }
-        if (a.out8 != nullptr && t == 0) a.out8_scale[row] = __fdiv_rn(tot.y * rstd, 127.f);
+        if (kAhead) cur = next;
+        else if (row + step < a.n_tok) fetch(cur, row + step);
     }
 }
 
@@ -188,12 +211,12 @@ __global__ void __launch_bounds__(512) quantize_i8_kernel(const uint16_t* __rest
     }
 }
 
-template <int V, bool kWarpRow>
-cudaError_t launch_norm(const BlockNormArgs& a, int threads, cudaStream_t stream) {
+template <int V, bool kWarpRow, bool kAhead>
+cudaError_t launch_norm(const BlockNormArgs& a, int threads, int resident, cudaStream_t stream) {
     const int per = kWarpRow ? threads / 32 : 1;
     const long want = (static_cast<long>(a.n_tok) + per - 1) / per;
-    const long most = 148L * (2048 / threads) * 4;
-    return launch_pdl(block_norm_kernel<V, kWarpRow>, dim3(static_cast<unsigned>(want < most ? want : most)),
+    const long most = 148L * resident;
+    return launch_pdl(block_norm_kernel<V, kWarpRow, kAhead>, dim3(static_cast<unsigned>(want < most ? want : most)),
                       dim3(threads), 0, stream, a);
 }
 
@@ -201,10 +224,13 @@ cudaError_t launch_norm(const BlockNormArgs& a, int threads, cudaStream_t stream
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
     const int nv = a.d / 8;
-    if (nv <= 32) return launch_norm<1, true>(a, 256, stream);
-    if (nv <= 64) return launch_norm<2, true>(a, 256, stream);
-    if (nv <= 1024) return launch_norm<1, false>(a, (nv + 31) / 32 * 32, stream);
-    return launch_norm<2, false>(a, (nv + 63) / 64 * 32, stream);
+    // blocks that an SM holds at the kernels' registers
+    if (nv <= 32) return launch_norm<1, true, true>(a, 256, 3, stream);
+    if (nv <= 64) return launch_norm<2, true, true>(a, 256, 2, stream);
+    const int threads = ((nv <= 1024 ? (nv + 1) / 2 : (nv + 3) / 4) + 31) / 32 * 32;
+    const int fit = 65536 / (threads * 96);
+    if (nv <= 1024) return launch_norm<2, false, true>(a, threads, fit > 0 ? fit : 1, stream);
+    return launch_norm<4, false, false>(a, threads, 1, stream);
 }
 
 cudaError_t launch_quantize_i8(const uint16_t* x, long ld_x, int n_rows, int d, int8_t* x8, float* scale,

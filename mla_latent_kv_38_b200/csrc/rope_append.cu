@@ -186,12 +186,14 @@ cudaError_t launch_rope_append(uint16_t* q_r, const uint16_t* k_r, const uint16_
                       static_cast<int>(q_blocks), status);
 }
 
-// mla_norm_rope_append: the append from the projections' rows.  The same two
-// kinds of blocks: [0, q_blocks) split the query rows (n_h, d_h + d_r), a
-// thread per 8 values -- a copy into q_c, or four rotated pairs into q_r -- and
-// the rest append, one warp per token: a lane holds 16 latent values, the sum
-// of squares is a warp reduction, and the key is rotated as above.  Bound by
-// memory: every byte read once and written once.
+// mla_norm_rope_append: the append from the projections' rows.  Blocks
+// [0, a_blocks) append, one warp per token: a lane holds 16 latent values, the
+// sum of squares is a warp reduction, and the key is rotated as above.  The
+// others split query rows, q_chunks blocks per token: the token's items are
+// first its heads' copies into q_c (8 values each), then its groups of four
+// rotated pairs into q_r, so that a warp does one kind and both outputs are
+// written in order; a thread loads its kItems items before it stores any.
+// Bound by memory: every byte read once and written once.
 struct NormAppendArgs {
     const uint16_t* q;
     const uint16_t* kv;
@@ -205,54 +207,74 @@ struct NormAppendArgs {
     int32_t* status;
     long ld_kv;
     float eps;
-    int max_pos, max_blocks, num_blocks, n_tok, T_q, n_h, d_c, d_h, d_r, block_size, q_blocks;
+    int max_pos, max_blocks, num_blocks, n_tok, T_q, n_h, d_c, d_h, d_r, block_size, a_blocks, q_chunks;
 };
+
+constexpr int kItems = 4;
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(256) norm_rope_append_kernel(const NormAppendArgs a) {
     griddep_launch_dependents();
     griddep_wait();   // the projections, the pool and the outputs may be in use by earlier kernels
     const int h = a.d_r >> 1;
-    if (static_cast<int>(blockIdx.x) < a.q_blocks) {
-        const int copies = a.d_h >> 3, items = copies + (a.d_r >> 3);
-        const long g = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
-        if (g >= static_cast<long>(a.n_tok) * a.n_h * items) return;
-        const long ni = g / items;                      // token * n_h + head
-        const int item = static_cast<int>(g - ni * items);
-        const int n = static_cast<int>(ni / a.n_h);
+    if (static_cast<int>(blockIdx.x) >= a.a_blocks) {
+        const unsigned qb = blockIdx.x - a.a_blocks;
+        const unsigned n = qb / a.q_chunks;
         const int p = a.positions[n];
         if (p < 0 || p >= a.max_pos || p / a.block_size >= a.max_blocks) return;   // flagged by the append
-        const uint16_t* src = a.q + ni * (a.d_h + a.d_r);
-        if (item < copies) {
-            reinterpret_cast<uint4*>(a.q_c + ni * a.d_h)[item] = reinterpret_cast<const uint4*>(src)[item];
-            return;
-        }
-        src += a.d_h;
-        const int m = 4 * (item - copies);
-        const float4 c = *reinterpret_cast<const float4*>(a.table + static_cast<size_t>(p) * a.d_r + m);
-        const float4 sn = *reinterpret_cast<const float4*>(a.table + static_cast<size_t>(p) * a.d_r + h + m);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(src + m);
-        const uint2 x2 = *reinterpret_cast<const uint2*>(src + h + m);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-        const uint32_t a_in[2] = {x1.x, x1.y}, b_in[2] = {x2.x, x2.y};
-        uint32_t a_out[2], b_out[2];
+        const unsigned per_c = a.d_h >> 3, per_r = a.d_r >> 3;           // items of one head
+        const unsigned copies = a.n_h * per_c, items = copies + a.n_h * per_r;
+        const unsigned first = (qb - n * a.q_chunks) * (kItems * 256) + threadIdx.x;
+        const uint16_t* src = a.q + static_cast<size_t>(n) * a.n_h * (a.d_h + a.d_r);
+        uint4 v[kItems];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            uint16_t y1[2], y2[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                rope_pair(static_cast<uint16_t>(a_in[w] >> (16 * e)), static_cast<uint16_t>(b_in[w] >> (16 * e)),
-                          cc[2 * w + e], ss[2 * w + e], &y1[e], &y2[e]);
-            a_out[w] = y1[0] | (static_cast<uint32_t>(y1[1]) << 16);
-            b_out[w] = y2[0] | (static_cast<uint32_t>(y2[1]) << 16);
+        for (int k = 0; k < kItems; ++k) {
+            const unsigned i = first + 256 * k;
+            if (i < copies) {
+                const unsigned head = i / per_c;
+                v[k] = *reinterpret_cast<const uint4*>(src + head * (a.d_h + a.d_r) + 8 * (i - head * per_c));
+            } else if (i < items) {
+                const unsigned head = (i - copies) / per_r, m = 4 * (i - copies - head * per_r);
+                const uint16_t* s = src + head * (a.d_h + a.d_r) + a.d_h + m;
+                const uint2 x1 = *reinterpret_cast<const uint2*>(s);
+                const uint2 x2 = *reinterpret_cast<const uint2*>(s + h);
+                v[k] = make_uint4(x1.x, x1.y, x2.x, x2.y);
+            }
         }
-        uint16_t* dst = a.q_r + ni * a.d_r;
-        *reinterpret_cast<uint2*>(dst + m) = make_uint2(a_out[0], a_out[1]);
-        *reinterpret_cast<uint2*>(dst + h + m) = make_uint2(b_out[0], b_out[1]);
+        uint4* q_c = reinterpret_cast<uint4*>(a.q_c) + static_cast<size_t>(n) * copies;
+        uint16_t* q_r = a.q_r + static_cast<size_t>(n) * a.n_h * a.d_r;
+        const float* cs = a.table + static_cast<size_t>(p) * a.d_r;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const unsigned i = first + 256 * k;
+            if (i < copies) {
+                q_c[i] = v[k];
+            } else if (i < items) {
+                const unsigned head = (i - copies) / per_r, m = 4 * (i - copies - head * per_r);
+                const float4 c = *reinterpret_cast<const float4*>(cs + m);
+                const float4 sn = *reinterpret_cast<const float4*>(cs + h + m);
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+                const uint32_t a_in[2] = {v[k].x, v[k].y}, b_in[2] = {v[k].z, v[k].w};
+                uint32_t a_out[2], b_out[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    uint16_t y1[2], y2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        rope_pair(static_cast<uint16_t>(a_in[w] >> (16 * e)), static_cast<uint16_t>(b_in[w] >> (16 * e)),
+                                  cc[2 * w + e], ss[2 * w + e], &y1[e], &y2[e]);
+                    a_out[w] = y1[0] | (static_cast<uint32_t>(y1[1]) << 16);
+                    b_out[w] = y2[0] | (static_cast<uint32_t>(y2[1]) << 16);
+                }
+                uint16_t* dst = q_r + head * a.d_r + m;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(a_out[0], a_out[1]);
+                *reinterpret_cast<uint2*>(dst + h) = make_uint2(b_out[0], b_out[1]);
+            }
+        }
         return;
     }
 
-    const int n = (blockIdx.x - a.q_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int n = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (n >= a.n_tok) return;
     const int b = n / a.T_q;
@@ -322,8 +344,8 @@ cudaError_t launch_norm_rope_append(const uint16_t* q, const uint16_t* kv, long 
                                     int n_tok, int T_q, int n_h, int d_c, int d_h, int d_r, int block_size,
                                     uint16_t* q_c, uint16_t* q_r, int32_t* status, cudaStream_t stream) {
     const int threads = 256, warps = threads / 32;
-    const long q_threads = q != nullptr ? static_cast<long>(n_tok) * n_h * ((d_h + d_r) / 8) : 0;
-    const long q_blocks = (q_threads + threads - 1) / threads;
+    const long q_chunks = (static_cast<long>(n_h) * ((d_h + d_r) / 8) + kItems * threads - 1) / (kItems * threads);
+    const long q_blocks = q != nullptr ? n_tok * q_chunks : 0;
     const long a_blocks = (n_tok + warps - 1) / warps;
     if (q_blocks + a_blocks > 0x7fffffffL) return cudaErrorInvalidValue;
     NormAppendArgs a;
@@ -331,7 +353,7 @@ cudaError_t launch_norm_rope_append(const uint16_t* q, const uint16_t* kv, long 
     a.pool = static_cast<unsigned char*>(pool), a.q_c = q_c, a.q_r = q_r, a.status = status;
     a.ld_kv = ld_kv, a.eps = eps, a.max_pos = max_pos, a.max_blocks = max_blocks, a.num_blocks = num_blocks;
     a.n_tok = n_tok, a.T_q = T_q, a.n_h = n_h, a.d_c = d_c, a.d_h = d_h, a.d_r = d_r, a.block_size = block_size;
-    a.q_blocks = static_cast<int>(q_blocks);
+    a.a_blocks = static_cast<int>(a_blocks), a.q_chunks = static_cast<int>(q_chunks);
     const dim3 grid(static_cast<unsigned>(q_blocks + a_blocks));
     return launch_pdl(e4m3 ? norm_rope_append_kernel<true> : norm_rope_append_kernel<false>, grid, dim3(threads), 0,
                       stream, a);
