@@ -66,8 +66,8 @@ constexpr int kThreads = 384;   // 12 warps: S loads, S MMAs, P.V MMAs, V loads,
 // Registers per thread: 168 at launch (65,536 / 384, rounded down to 8); then
 // the load / MMA warpgroup gives registers up to the two softmax warpgroups.
 constexpr uint32_t kRegsLaunch = 168;
-constexpr uint32_t kRegsIssue = 64;
-constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsIssue = 80;
+constexpr uint32_t kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr int kClusters = 74;                     // 148 SMs / 2
 constexpr int kDc = 512, kDr = 64, kRow = 576;    // row = c^KV || k^R
@@ -112,13 +112,15 @@ enum {
     BAR_VR_EMPTY = BAR_VR_FULL + kVRing,
     BAR_S_FULL = BAR_VR_EMPTY + kVRing,      // + S buffer
     BAR_S_FREE = BAR_S_FULL + 2,             // + S buffer (leader, 8 warps x 2 CTAs)
-    BAR_P_FULL = BAR_S_FREE + 2,             // + P half (leader, 4 warps x 2 CTAs)
+    BAR_P_FULL = BAR_S_FREE + 2,             // + P half (leader, 4 warps x 2 CTAs; half 0: all 8 x 2)
     BAR_P_FREE = BAR_P_FULL + 2,             // + P half (each CTA, MMA commit)
     BAR_TAIL_READY = BAR_P_FREE + 2,         // each CTA, MMA thread arrives remotely
     BAR_TAIL_DONE = BAR_TAIL_READY + 1,      // leader, 8 warps x 2 CTAs
     BAR_DRAIN = BAR_TAIL_DONE + 1,           // S issuer's own drain on abort
     BAR_DRAIN_PV = BAR_DRAIN + 1,            // P.V issuer's
-    NUM_BARS = BAR_DRAIN_PV + 1
+    BAR_X_FREE = BAR_DRAIN_PV + 1,           // + row group: its 4 warps have read the exchanged values
+    BAR_X_FULL = BAR_X_FREE + 2,             // + row group: its 4 warps have written them
+    NUM_BARS = BAR_X_FULL + 2
 };
 static_assert(NUM_BARS <= static_cast<int>(kMaxBars), "barrier area");
 
@@ -178,12 +180,13 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
     return v;
 }
 
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint32_t addr, uint32_t parity, volatile int* abort_flag,
                                          int32_t* status, uint64_t timeout_ns) {
-    if (ptx::mbar_try_wait(addr, parity)) return true;
+    if (ptx::mbar_try_wait<kCluster>(addr, parity)) return true;
     const uint64_t t0 = ptx::global_timer_ns();
     while (true) {
-        if (ptx::mbar_try_wait_suspend(addr, parity, kSuspendHintNs)) return true;
+        if (ptx::mbar_try_wait_suspend<kCluster>(addr, parity, kSuspendHintNs)) return true;
         if (*abort_flag) return false;
         if (ptx::global_timer_ns() - t0 > timeout_ns) {
             *abort_flag = 1;
@@ -571,13 +574,17 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             ptx::mbar_init(bar(BAR_S_FREE + b), 16);   // 8 softmax warps x 2 CTAs
         }
         for (int hf = 0; hf < 2; ++hf) {
-            ptx::mbar_init(bar(BAR_P_FULL + hf), 8);   // 4 softmax warps x 2 CTAs
+            ptx::mbar_init(bar(BAR_P_FULL + hf), hf == 0 ? 16 : 8);   // softmax warps of both CTAs
             ptx::mbar_init(bar(BAR_P_FREE + hf), 1);
         }
         ptx::mbar_init(bar(BAR_TAIL_READY), 1);
         ptx::mbar_init(bar(BAR_TAIL_DONE), 16);
         ptx::mbar_init(bar(BAR_DRAIN), 1);
         ptx::mbar_init(bar(BAR_DRAIN_PV), 1);
+        for (int g = 0; g < 2; ++g) {
+            ptx::mbar_init(bar(BAR_X_FREE + g), 4);
+            ptx::mbar_init(bar(BAR_X_FULL + g), 4);
+        }
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -876,7 +883,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                                     break;
                                 ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(BAR_TAIL_READY), 0));
                                 ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(BAR_TAIL_READY), 1));
-                                if (!(ok = wait_bar(bar(BAR_TAIL_DONE), tails & 1, abort_flag, p.status, tmo))) break;
+                                if (!(ok = wait_bar<true>(bar(BAR_TAIL_DONE), tails & 1, abort_flag, p.status, tmo))) break;
                                 ++tails;
                             }
                             if (!(ok = wait_bar(bar(BAR_VR_FULL + e % kVRing), (e / kVRing) & 1, abort_flag, p.status, tmo)))
@@ -933,9 +940,23 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         // this thread's row of the unit and the row's token in a unit of several
         const int unit_row = 64 * static_cast<int>(rank) + m;
         const int row_tok = kShared ? unit_row / p.um.n_h : 0;
-        // the four partial values of row m (both key halves, both column groups)
-        auto row_max4 = [&]() {
-            return fmaxf(fmaxf(xmax[m], xmax[64 + m]), fmaxf(xmax[128 + m], xmax[192 + m]));
+        // The four partial values of row m (both key halves, both column groups)
+        // meet through shared memory: the four warps of 32 rows (group wq & 1)
+        // write, wait for each other and read; a warp writes again only when all
+        // four have read, which is long past by then.
+        const int xg = wq & 1;
+        int x_turn = 0;
+        auto exchange = [&](float v, bool sum) {
+            ok = wait_bar(bar(BAR_X_FREE + xg), (x_turn & 1) ^ 1, abort_flag, p.status, tmo);
+            xmax[cg * 128 + l] = v;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_X_FULL + xg));
+            ok = ok && wait_bar(bar(BAR_X_FULL + xg), x_turn & 1, abort_flag, p.status, tmo);
+            ++x_turn;
+            const float a = xmax[m], b = xmax[64 + m], c = xmax[128 + m], d = xmax[192 + m];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_X_FREE + xg));
+            return sum ? a + b + c + d : fmaxf(fmaxf(a, b), fmaxf(c, d));
         };
         while (ok && !w.done()) {
             const Tile t = w.next();
@@ -950,27 +971,28 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             ok = wait_bar(bar(BAR_S_FULL + sb), (i >> 1) & 1, abort_flag, p.status, tmo);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             ptx::tc_fence_after();
-            // This thread's 64 scores (row m, keys key0 ..) are read from tensor
-            // memory twice: once for the row maximum, once for the weights.
+            // this thread's 64 scores (row m, keys key0 ..)
             const uint32_t s_col = t_lane + kTmemS + 128 * sb + 64 * cg;
             const int key0 = kPage * t.page0 + (hi ? 128 : 0) + 64 * cg;
             const int nvalid = key_end - key0;   // scores of this thread that count (<= 0 .. >= 64)
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // independent chains
-            {
-                uint32_t r[2][32];
-                ptx::tmem_ld32(s_col, r[0]);
-                ptx::tmem_ld32(s_col + 32, r[1]);
-                ptx::tmem_wait_ld();
+            uint32_t r[2][32];
+            ptx::tmem_ld32(s_col, r[0]);
+            ptx::tmem_ld32(s_col + 32, r[1]);
+            ptx::tmem_wait_ld();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(BAR_S_FREE + sb));
+            if (nvalid < 64) {   // masked scores
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
-                    if (j < nvalid) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j >> 5][j & 31]));
+                    if (j >= nvalid) r[j >> 5][j & 31] = __float_as_uint(-INFINITY);
             }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // independent chains
+#pragma unroll
+            for (int j = 0; j < 64; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j >> 5][j & 31]));
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            mx *= p.scale_log2;   // the scale is positive
-            xmax[cg * 128 + l] = mx;
-            ptx::named_bar_sync(1, 256);
-            mx = row_max4();
-            ptx::named_bar_sync(2, 256);   // every read done before the buffer is written again
+            mx = exchange(mx * p.scale_log2, false);   // the scale is positive
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             float new_m = m_used;
             bool resc = false;
             if (mx > m_used + kRescaleThreshold) {
@@ -982,50 +1004,46 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             if (kShared && new_m == -INFINITY) alpha = 1.f;
             m_used = new_m;
 
-            // The weights of row m, keys key0 + [0, 64): computed into registers
-            // first, which ends this thread's reads of the S buffer.
+            // The weights of row m, keys key0 + [0, 64) (a masked score's is 2^-inf = 0).
             float ps2[2] = {0.f, 0.f};
             const float neg_m = kShared && m_used == -INFINITY ? 0.f : -m_used;
             uint32_t pk[32];
-            {
-                uint32_t r[2][32];
-                ptx::tmem_ld32(s_col, r[0]);
-                ptx::tmem_ld32(s_col + 32, r[1]);
-                ptx::tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                    const float s0 = __uint_as_float(r[j >> 5][j & 31]), s1 = __uint_as_float(r[j >> 5][(j & 31) + 1]);
-                    const float p0 = j < nvalid ? ex2(fmaf(s0, p.scale_log2, neg_m)) : 0.f;
-                    const float p1 = j + 1 < nvalid ? ex2(fmaf(s1, p.scale_log2, neg_m)) : 0.f;
-                    ps2[(j >> 1) & 1] += p0 + p1;
-                    pk[j >> 1] = pack_bf16x2(p0, p1);
-                }
+            for (int j = 0; j < 64; j += 2) {
+                const float s0 = __uint_as_float(r[j >> 5][j & 31]), s1 = __uint_as_float(r[j >> 5][(j & 31) + 1]);
+                const float p0 = ex2(fmaf(s0, p.scale_log2, neg_m)), p1 = ex2(fmaf(s1, p.scale_log2, neg_m));
+                ps2[(j >> 1) & 1] += p0 + p1;
+                pk[j >> 1] = pack_bf16x2(p0, p1);
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(BAR_S_FREE + sb));
             const float ps = ps2[0] + ps2[1];
             l_part = l_part * alpha + ps;
 
             // This half of the P buffer must be free (the previous tile's P.V MMAs on
-            // it complete); a rescale of O needs the whole previous P.V complete.
+            // it complete); a rescale of O needs the whole previous P.V complete, and
+            // half 0's MMAs, which add to every lane of O, need the rescale of all
+            // warps: those of half 1 arrive at P_FULL + 0 too.
             const int hf = hi ? 1 : 0;
-            ok = wait_bar(bar(BAR_P_FREE + hf), (i & 1) ^ 1, abort_flag, p.status, tmo);
-            if (ok && !hi && __any_sync(0xffffffffu, resc))
-                ok = wait_bar(bar(BAR_P_FREE + 1), (i & 1) ^ 1, abort_flag, p.status, tmo);
+            const bool any_resc = __any_sync(0xffffffffu, resc);
+            ok = wait_bar(bar(BAR_P_FREE + 0), (i & 1) ^ 1, abort_flag, p.status, tmo);
+            if (hi && !any_resc && ok && lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(BAR_P_FULL + 0));
+            if (ok && (hi || any_resc)) ok = wait_bar(bar(BAR_P_FREE + 1), (i & 1) ^ 1, abort_flag, p.status, tmo);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             ptx::tc_fence_after();
-            if (resc) {
+            if (any_resc) {   // (alpha is 1 where the row keeps its maximum)
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t o[32];
                     ptx::tmem_ld32(t_lane + kTmemO + 128 * cg + 32 * q, o);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                    for (int c = 0; c < 32; ++c)
+                        o[c] = resc ? __float_as_uint(__uint_as_float(o[c]) * alpha) : o[c];
                     ptx::tmem_st32(t_lane + kTmemO + 128 * cg + 32 * q, o);
                 }
                 ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (hi && lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(BAR_P_FULL + 0));
             }
             // P row m, keys key0 + [0, 64) = one 64-key block (2 hi + cg) of P:
             // K-major, 128-byte rows, 128-byte swizzle (16-byte chunk index XOR row & 7)
@@ -1039,7 +1057,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(BAR_P_FULL + hf));
+            if (lane == 0) ptx::mbar_arrive_cluster_own(leader_bar(BAR_P_FULL + hf));
 
             // V ring position of this tile's entries (one per page)
             const int v_start = v_before;
@@ -1048,7 +1066,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 if (!tail_page<kShared>(t, pg)) continue;
                 // zero the rows past the end in this CTA's V entry of the page
                 // (4 chunks of 64 rows x 128 B)
-                ok = wait_bar(bar(BAR_TAIL_READY), tails & 1, abort_flag, p.status, tmo);
+                ok = wait_bar<true>(bar(BAR_TAIL_READY), tails & 1, abort_flag, p.status, tmo);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ++tails;
                 const int left = t.kv - kPage * (t.page0 + pg);   // keys from the page's first row on
@@ -1090,10 +1108,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 ok = wait_bar(bar(BAR_P_FREE + 1), i & 1, abort_flag, p.status, tmo);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
-                xmax[cg * 128 + l] = l_part;   // partial row sums
-                ptx::named_bar_sync(1, 256);
-                const float lsum = xmax[m] + xmax[64 + m] + xmax[128 + m] + xmax[192 + m];
-                ptx::named_bar_sync(2, 256);
+                const float lsum = exchange(l_part, true);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
                 const float lse = lsum > 0.f ? (m_used + __log2f(lsum)) * kLn2 : -INFINITY;
                 const bool whole = t.whole && !(kShared && p.um.n_prefix > 0);
