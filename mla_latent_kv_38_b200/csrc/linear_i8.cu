@@ -154,21 +154,25 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
             }
             if (!__all_sync(0xffffffffu, ok)) break;
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         bool ok = true;
         for (int c = 0; c < c1 - c0 && ok; ++c) {
             const int s = c % S;
-            ok = wait_bounded(full(s), (c / S) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, wait_bounded(full(s), (c / S) & 1, abort_flag, p.status));
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t st = sbase + s * stage_bytes;
+            if (ptx::elect_one()) {
+                const uint32_t st = sbase + s * stage_bytes;
+                const uint64_t a = ptx::smem_desc_sw128(st, 16, 1024), b = ptx::smem_desc_sw128(st + kOpBytes, 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                ptx::mma1_i8_ss(tmem, ptx::smem_desc_sw128(st + kk * 32, 16, 1024),
-                                ptx::smem_desc_sw128(st + kOpBytes + kk * 32, 16, 1024), p.idesc, (c | kk) ? 1u : 0u);
-            ptx::mma1_commit(empty(s));
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma1_i8_ss(tmem, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), p.idesc, (c | kk) ? 1u : 0u);
+                ptx::mma1_commit(empty(s));
+            }
+            __syncwarp();
         }
-        ptx::mma1_commit(done);   // completes when every MMA issued above has (also on the abort path)
+        // completes when every MMA issued above has (also on the abort path)
+        if (ptx::elect_one()) ptx::mma1_commit(done);
     }
     __syncwarp();
     wait_bounded(done, 0, abort_flag, p.status);
@@ -302,30 +306,37 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int e = 0, i = 0;
             bool ok = true;
             for (int t = cluster; t < p.tiles && ok; t += clusters, ++i) {
                 const int b = i & 1;
-                if (!(ok = wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status))) break;
+                ok = __all_sync(0xffffffffu, wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status));
+                if (!ok) break;
                 ptx::tc_fence_after();
                 for (int c = 0; c < p.chunks; ++c, ++e) {
                     const int s = e % kWideStages;
-                    if (!(ok = wait_bounded(bar(W_FULL + s), (e / kWideStages) & 1, abort_flag, p.status))) break;
+                    ok = __all_sync(0xffffffffu, wait_bounded(bar(W_FULL + s), (e / kWideStages) & 1, abort_flag, p.status));
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t st = sbase + s * kWideStage;
+                    if (ptx::elect_one()) {
+                        const uint32_t st = sbase + s * kWideStage;
+                        const uint64_t a = ptx::smem_desc_sw128(st, 16, 1024),
+                                       w = ptx::smem_desc_sw128(st + kOpBytes, 16, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_pair_i8_ss(tmem + 256 * b, ptx::smem_desc_sw128(st + kk * 32, 16, 1024),
-                                            ptx::smem_desc_sw128(st + kOpBytes + kk * 32, 16, 1024), kWideIdesc,
-                                            (c | kk) ? 1u : 0u);
-                    ptx::mma_commit_pair(bar(W_EMPTY + s), 0x3);
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_pair_i8_ss(tmem + 256 * b, a + ((32 * kk) >> 4), w + ((32 * kk) >> 4), kWideIdesc,
+                                                (c | kk) ? 1u : 0u);
+                        ptx::mma_commit_pair(bar(W_EMPTY + s), 0x3);
+                        if (c == p.chunks - 1) ptx::mma_commit_pair(bar(W_ACC_FULL + b), 0x3);
+                    }
+                    __syncwarp();
                 }
-                if (ok) ptx::mma_commit_pair(bar(W_ACC_FULL + b), 0x3);
             }
             if (!ok) {
-                // let every MMA this thread issued finish before the teardown frees anything
-                ptx::mma_commit_pair(bar(W_DRAIN), 0x1);
+                // let every MMA this warp issued finish before the teardown frees anything
+                if (ptx::elect_one()) ptx::mma_commit_pair(bar(W_DRAIN), 0x1);
+                __syncwarp();
                 const uint64_t t0 = ptx::global_timer_ns();
                 while (!ptx::mbar_try_wait(bar(W_DRAIN), 0) && ptx::global_timer_ns() - t0 < kTimeoutNs) {
                 }

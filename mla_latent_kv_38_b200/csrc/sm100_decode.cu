@@ -238,7 +238,7 @@ __device__ __forceinline__ int unit_keys(const int32_t* seq_lens, int u, const U
         return L - um.T_q + min(um.T_q, (x.t + 1) * um.tok_per_unit) - (um.n_prefix > 0 ? own0 : 0);
     } else {
         const UnitIdx x = unit_index(u, um.n_hb, um.B);
-        const int L = seq_lens[x.b];   // global or shared memory
+        const int L = seq_lens[x.b];
         return (L >= um.T_q && L <= um.max_blocks * kPage) ? L - um.T_q + x.t + 1 : 0;
     }
 }
@@ -250,15 +250,23 @@ __device__ __forceinline__ bool first_of_sequence(int u, const UnitMap& um) {
     return u >= 0 && u < um.B * um.n_hb && u % um.n_hb == 0;
 }
 
-// Last unit v with pf[v] <= g (for g < T: the unit holding page g).
-__device__ __forceinline__ int unit_of_page(const int32_t* pf, int U, int g) {
-    int lo = 0, hi = U - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pf[mid] <= g) lo = mid; else hi = mid - 1;
+// Last of n entries with a[v] <= g (a ascending, a[0] <= g), narrowed to an
+// eighth with each round of independent loads.
+__device__ __forceinline__ int last_at_or_below(const int32_t* a, int n, int g) {
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 7) >> 3;
+        int k = 0;
+#pragma unroll
+        for (int j = 1; j < 8; ++j) k += j * step < n && a[lo + j * step] <= g;
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     return lo;
 }
+
+// Last unit v with pf[v] <= g (for g < T: the unit holding page g).
+__device__ __forceinline__ int unit_of_page(const int32_t* pf, int U, int g) { return last_at_or_below(pf, U, g); }
 
 // Work is cut at whole tiles (4 pages, 256 keys, counted from each unit's
 // start), so that a range that crosses a unit boundary carries no extra
@@ -337,19 +345,11 @@ __device__ void compute_cuts(int* cuts, int* tmp, const int32_t* pf, const int32
 }
 
 // Cluster whose range holds page g < T (the last cluster starting at or before g).
-__device__ int cluster_of_page(int g, const int* cuts) {
-    int lo = 0, hi = kClusters - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cuts[mid] <= g) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
+__device__ __forceinline__ int cluster_of_page(int g, const int* cuts) { return last_at_or_below(cuts, kClusters, g); }
 
 // Merge metadata of unit u: {kv_len, first cluster, parts, sequence}.
 template <bool kShared>
-__device__ int4 unit_meta_of(int u, const int32_t* pf, const int* cuts, const int32_t* seq_lens, const UnitMap& um) {
-    const int kv = unit_keys<kShared>(seq_lens, u, um);
+__device__ int4 unit_meta_of(int u, const int32_t* pf, const int* cuts, int kv, const UnitMap& um) {
     const int b = kShared ? 0 : unit_index(u, um.n_hb, um.B).b;
     const int a = pf[u], e = pf[u + 1];
     if (e <= a) return make_int4(0, 0, 0, b);
@@ -472,17 +472,20 @@ struct TileWalker {
 };
 
 // Block-wide exclusive scans of the units' page counts, tile counts and cut
-// costs into pf, tf, wf[0 .. U] (U <= kInKernelUnits); every thread of the
+// costs into pf, tf, wf[0 .. U] (U <= kInKernelUnits), and the units' key
+// counts into kvs; every thread of the
 // CTA takes part; warp_tot holds 3 x 16 ints of scratch.  Returns {T, Tt}.
 template <bool kShared>
-__device__ int2 schedule_scan(int* pf, int* tf, int* wf, int* warp_tot, const int32_t* seq_lens, int U,
+__device__ int2 schedule_scan(int* pf, int* tf, int* wf, int* kvs, int* warp_tot, const int32_t* seq_lens, int U,
                               const UnitMap& um) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int per = (U + kThreads - 1) / kThreads;
     const int beg = min(U, tid * per), end = min(U, beg + per);
     int loc[3] = {0, 0, 0};
     for (int u = beg; u < end; ++u) {
-        const int pages = (unit_keys<kShared>(seq_lens, u, um) + kPage - 1) / kPage;
+        const int kv = unit_keys<kShared>(seq_lens, u, um);
+        kvs[u] = kv;
+        const int pages = (kv + kPage - 1) / kPage;
         const int tiles = (pages + kTilePages - 1) / kTilePages;
         pf[u + 1] = pages;
         tf[u + 1] = tiles;
@@ -633,11 +636,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         int* tfx = sc + kInKernelUnits + 1;                           // tile prefix, U + 1
         int* wfx = tfx + kInKernelUnits + 1;                          // cost prefix, U + 1
         int* ctmp = wfx + kInKernelUnits + 1;                         // cut scratch, C + 1
-        int* lens = ctmp + kClusters + 1;                             // sequence lengths, B <= U
-        int* wtot = lens + kInKernelUnits;                            // scan scratch, 48
-        for (int b = threadIdx.x; b < p.um.B; b += kThreads) lens[b] = __ldg(p.seq_lens + b);
-        __syncthreads();
-        const int2 TT = schedule_scan<kShared>(sc, tfx, wfx, wtot, lens, p.U, p.um);
+        int* kvx = ctmp + kClusters + 1;                              // key counts, U
+        int* wtot = kvx + kInKernelUnits;                             // scan scratch, 48
+        const int2 TT = schedule_scan<kShared>(sc, tfx, wfx, kvx, wtot, p.seq_lens, p.U, p.um);
         const int T = TT.x;
         int* cuts = reinterpret_cast<int*>(smem + kOffCuts);
         compute_cuts(cuts, ctmp, sc, tfx, wfx, p.U, T, TT.y, p.max_splits);
@@ -653,12 +654,12 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 kv_base = dst;
             }
             for (int k = threadIdx.x; k <= u1 - u0; k += kThreads)
-                dst[k] = unit_keys<kShared>(lens, u0 + k, p.um);
+                dst[k] = kvx[u0 + k];
         }
         kv_off = u0;
         // merge metadata and length checks, spread over the grid's threads
         for (int u = blockIdx.x * kThreads + threadIdx.x; u < p.U; u += gridDim.x * kThreads) {
-            const int4 m = unit_meta_of<kShared>(u, sc, cuts, lens, p.um);
+            const int4 m = unit_meta_of<kShared>(u, sc, cuts, kvx[u], p.um);
             p.unit_meta[u] = m;
             if (m.x == 0 && first_of_sequence<kShared>(u, p.um)) raise_status(p.status, MLA_STATUS_BAD_SEQ_LEN);
         }
@@ -812,7 +813,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         } else if (warp == 1) {
             // ------------------------------------------------------------ S = Q K^T issuer
             // S(i) occupies entries 9 i .. 9 i + 8 of the S ring (keys as B, query as A).
-            if (rank == 0 && lane == 0 && g0 < g1) {
+            // The whole warp runs the loop, one lane issues (see elect_one).
+            if (rank == 0 && g0 < g1) {
                 TileWalker<kShared> w;
                 walker(w);
                 int i = 0;
@@ -821,30 +823,35 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                     w.next();
                     const int e0 = kChunks * i;
                     const int sb = i & 1;
-                    if (!(ok = wait_bar(bar(BAR_S_FREE + sb), ((i >> 1) & 1) ^ 1, abort_flag, p.status, tmo))) break;
+                    ok = __all_sync(0xffffffffu, wait_bar(bar(BAR_S_FREE + sb), ((i >> 1) & 1) ^ 1, abort_flag, p.status, tmo));
+                    if (!ok) break;
                     ptx::tc_fence_after();   // the softmax's reads of this S buffer are done
                     for (int c = 0; c < kChunks; ++c) {
                         const int e = e0 + c;
-                        if (!(ok = wait_bar(bar(BAR_SR_FULL + e % kSRing), (e / kSRing) & 1, abort_flag, p.status, tmo)))
-                            break;
-                        const uint32_t ent = sbase + kOffSRing + (e % kSRing) * kSEntry;
-                        const uint64_t b0 = ptx::smem_desc_sw128(ent, 16, 1024);
-                        const uint64_t a0 = ptx::smem_desc_sw128(ent + 2 * kBox, 16, 1024);
-    #pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            const uint64_t a = a0 + static_cast<uint64_t>((32 * k4) >> 4);
-                            const uint64_t bd = b0 + static_cast<uint64_t>((32 * k4) >> 4);
-                            ptx::mma_pair_ss(tmem_base + kTmemS + 128 * sb, a, bd, kIdescS, (c | k4) ? 1u : 0u);
+                        ok = __all_sync(0xffffffffu, wait_bar(bar(BAR_SR_FULL + e % kSRing), (e / kSRing) & 1, abort_flag,
+                                                              p.status, tmo));
+                        if (!ok) break;
+                        if (ptx::elect_one()) {
+                            const uint32_t ent = sbase + kOffSRing + (e % kSRing) * kSEntry;
+                            const uint64_t b0 = ptx::smem_desc_sw128(ent, 16, 1024);
+                            const uint64_t a0 = ptx::smem_desc_sw128(ent + 2 * kBox, 16, 1024);
+#pragma unroll
+                            for (int k4 = 0; k4 < 4; ++k4) {
+                                const uint64_t a = a0 + static_cast<uint64_t>((32 * k4) >> 4);
+                                const uint64_t bd = b0 + static_cast<uint64_t>((32 * k4) >> 4);
+                                ptx::mma_pair_ss(tmem_base + kTmemS + 128 * sb, a, bd, kIdescS, (c | k4) ? 1u : 0u);
+                            }
+                            ptx::mma_commit_pair(bar(BAR_SR_EMPTY + e % kSRing), 0x3);
+                            if (c == kChunks - 1) ptx::mma_commit_pair(bar(BAR_S_FULL + sb), 0x3);
                         }
-                        ptx::mma_commit_pair(bar(BAR_SR_EMPTY + e % kSRing), 0x3);
+                        __syncwarp();
                     }
-                    if (!ok) break;
-                    ptx::mma_commit_pair(bar(BAR_S_FULL + sb), 0x3);
                     ++i;
                 }
                 if (!ok) {
-                    // let every MMA this thread issued finish before the teardown frees anything
-                    ptx::mma_commit_pair(bar(BAR_DRAIN), 0x1);
+                    // let every MMA this warp issued finish before the teardown frees anything
+                    if (ptx::elect_one()) ptx::mma_commit_pair(bar(BAR_DRAIN), 0x1);
+                    __syncwarp();
                     const uint64_t t0 = ptx::global_timer_ns();
                     while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::global_timer_ns() - t0 < tmo) {
                     }
@@ -854,7 +861,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             if (rank == 0) {
                 // -------------------------------------------------------- O += P V issuer
                 // V(i) occupies the next np entries of the V ring (one per page).
-                if (lane == 0 && g0 < g1) {
+                if (g0 < g1) {
                     TileWalker<kShared> w;
                     walker(w);
                     int i = 0, tails = 0, e = 0;
@@ -868,46 +875,57 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                         // MMAs complete.
                         for (int pg = 0; pg < 4 && ok; ++pg) {
                             if (pg == 0 || pg == 2) {
-                                if (pg == 2) ptx::mma_commit_pair(bar(BAR_P_FREE + 0), 0x3);
-                                if (!(ok = wait_bar(bar(BAR_P_FULL + (pg >> 1)), i & 1, abort_flag, p.status, tmo))) break;
+                                if (pg == 2) {
+                                    if (ptx::elect_one()) ptx::mma_commit_pair(bar(BAR_P_FREE + 0), 0x3);
+                                    __syncwarp();
+                                }
+                                ok = __all_sync(0xffffffffu, wait_bar(bar(BAR_P_FULL + (pg >> 1)), i & 1, abort_flag,
+                                                                      p.status, tmo));
+                                if (!ok) break;
                                 ptx::tc_fence_after();
                             }
                             if (pg >= t.np) continue;
+                            ok = __all_sync(0xffffffffu, wait_bar(bar(BAR_VR_FULL + e % kVRing), (e / kVRing) & 1, abort_flag,
+                                                                  p.status, tmo));
+                            if (!ok) break;
                             if (tail_page<kShared>(t, pg)) {
-                                // the page holds rows past the end: once its V
+                                // the page holds rows past the end: now that its V
                                 // entry has landed, the softmax warps of both CTAs zero those
                                 // rows (entries are consumed in ring order, so the earlier
                                 // pages' slots are already free for this load)
-                                if (!(ok = wait_bar(bar(BAR_VR_FULL + e % kVRing), (e / kVRing) & 1, abort_flag,
-                                                    p.status, tmo)))
-                                    break;
-                                ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(BAR_TAIL_READY), 0));
-                                ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(BAR_TAIL_READY), 1));
-                                if (!(ok = wait_bar<true>(bar(BAR_TAIL_DONE), tails & 1, abort_flag, p.status, tmo))) break;
+                                if (lane < 2) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(BAR_TAIL_READY), lane));
+                                __syncwarp();
+                                ok = __all_sync(0xffffffffu, wait_bar<true>(bar(BAR_TAIL_DONE), tails & 1, abort_flag,
+                                                                            p.status, tmo));
+                                if (!ok) break;
                                 ++tails;
                             }
-                            if (!(ok = wait_bar(bar(BAR_VR_FULL + e % kVRing), (e / kVRing) & 1, abort_flag, p.status, tmo)))
-                                break;
-                            for (int h = 0; h < 2; ++h) {
-                                const uint64_t b0 = ptx::smem_desc_sw128(
-                                    sbase + kOffVRing + (e % kVRing) * kVEntry + h * 2 * kBox, kBox, 1024);
-    #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    const uint64_t a = a0 + static_cast<uint64_t>((pg * kBox + 32 * kk) >> 4);
-                                    const uint64_t bd = b0 + static_cast<uint64_t>((2048 * kk) >> 4);
-                                    ptx::mma_pair_ss(tmem_base + kTmemO + 128 * h, a, bd, kIdescPV,
-                                                     (t.first && pg == 0 && kk == 0) ? 0u : 1u);
+                            if (ptx::elect_one()) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint64_t b0 = ptx::smem_desc_sw128(
+                                        sbase + kOffVRing + (e % kVRing) * kVEntry + h * 2 * kBox, kBox, 1024);
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk) {
+                                        const uint64_t a = a0 + static_cast<uint64_t>((pg * kBox + 32 * kk) >> 4);
+                                        const uint64_t bd = b0 + static_cast<uint64_t>((2048 * kk) >> 4);
+                                        ptx::mma_pair_ss(tmem_base + kTmemO + 128 * h, a, bd, kIdescPV,
+                                                         (t.first && pg == 0 && kk == 0) ? 0u : 1u);
+                                    }
                                 }
+                                ptx::mma_commit_pair(bar(BAR_VR_EMPTY + e % kVRing), 0x3);
                             }
-                            ptx::mma_commit_pair(bar(BAR_VR_EMPTY + e % kVRing), 0x3);
+                            __syncwarp();
                             ++e;
                         }
                         if (!ok) break;
-                        ptx::mma_commit_pair(bar(BAR_P_FREE + 1), 0x3);
+                        if (ptx::elect_one()) ptx::mma_commit_pair(bar(BAR_P_FREE + 1), 0x3);
+                        __syncwarp();
                         ++i;
                     }
                     if (!ok) {
-                        ptx::mma_commit_pair(bar(BAR_DRAIN_PV), 0x1);
+                        if (ptx::elect_one()) ptx::mma_commit_pair(bar(BAR_DRAIN_PV), 0x1);
+                        __syncwarp();
                         const uint64_t t0 = ptx::global_timer_ns();
                         while (!ptx::mbar_try_wait(bar(BAR_DRAIN_PV), 0) && ptx::global_timer_ns() - t0 < tmo) {
                         }
@@ -1299,7 +1317,7 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um
     __shared__ int cuts[kClusters + 1], cut_tmp[kClusters + 1];
     compute_cuts(cuts, cut_tmp, prefix, tprefix, wprefix, U, T, Tt, max_splits);
     for (int u = threadIdx.x; u < U; u += 1024) {
-        const int4 m = unit_meta_of<kShared>(u, prefix, cuts, seq_lens, um);
+        const int4 m = unit_meta_of<kShared>(u, prefix, cuts, kv_out[u], um);
         unit_meta[u] = m;
         if (m.x == 0 && first_of_sequence<kShared>(u, um)) raise_status(status, MLA_STATUS_BAD_SEQ_LEN);
     }

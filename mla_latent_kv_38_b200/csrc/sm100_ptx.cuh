@@ -228,6 +228,20 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// One lane of a converged warp, the same one every time.  MMAs issued under
+// this predicate by a warp that runs its loop converged take their descriptors
+// from uniform registers; under `lane == 0` every operand is moved there first,
+// which cost 66 to 140 cycles an MMA where the tensor core needs 32 to 64.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---- tcgen05 ----------------------------------------------------------------------
 
 // whole warp; writes the TMEM base address to smem `dst`
