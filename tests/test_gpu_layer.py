@@ -147,6 +147,55 @@ def test_linear_scales_beyond_float32_products(M):
     _check_linear(_linear(M, x8, sx, w8, sw), x8, sx, w8, sw)
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(129, 144, 15368), (300, 272, 7696), (1030, 144, 3336), (5000, 64, 1032),
+                                          (256, 2064, 15360), (2048, 16, 2056)])
+def test_linear_many_tokens(M, n, d_in, d_out):
+    """Enough output tiles for the many-token kernel, whole and ragged ones."""
+    g = _gen(n + d_in * 3 + d_out)
+    x8, w8 = _i8(g, n, d_in), _i8(g, d_out, d_in)
+    sx = torch.rand(n, generator=g, device="cuda") + 0.01
+    sw = torch.rand(d_out, generator=g, device="cuda") * 1e-3 + 1e-5
+    _check_linear(_linear(M, x8, sx, w8, sw), x8, sx, w8, sw)
+
+
+def test_linear_many_tokens_strided_and_extreme(M):
+    n, d_in = 300, 1040
+    wide = torch.full((n, d_in + 48), 5, dtype=torch.int8, device="cuda")
+    x8 = wide[:, 16:16 + d_in]
+    x8[:] = -128
+    w8 = torch.full((7696, d_in), -128, dtype=torch.int8, device="cuda")
+    w8[1::3] = 127
+    sx = torch.rand(n, generator=_gen(1), device="cuda") + 0.5
+    sw = torch.rand(7696, generator=_gen(2), device="cuda") + 0.5
+    _check_linear(_linear(M, x8, sx, w8, sw, ld=d_in + 48), x8, sx, w8, sw)
+
+
+def test_quantize_smallest_and_largest_rows(M):
+    """Rows whose 127 / max overflows float32, and rows at the top of the range."""
+    tiny = 2.0 ** -133
+    x = torch.zeros(4, 32, dtype=torch.float64, device="cuda")
+    x[0, :20] = torch.arange(-10, 10, device="cuda") * tiny
+    x[1, 3] = tiny
+    x[2, :] = torch.linspace(-1, 1, 32, device="cuda", dtype=torch.float64) * 2.0 ** -126
+    x[3, :] = torch.linspace(-1, 1, 32, device="cuda", dtype=torch.float64) * 3e38
+    x = x.bfloat16()
+    x8 = torch.empty(4, 32, dtype=torch.int8, device="cuda")
+    s = torch.empty(4, device="cuda")
+    M.mla_quantize_i8(x, 32, 4, 32, x8, s)
+    np.testing.assert_array_equal(x8.cpu().numpy(), _codes64(x)[0])
+
+
+@pytest.mark.parametrize("rows,d", [(700, 16), (3000, 1536), (2500, 2048), (700, 2056 + 8)])
+def test_quantize_many_rows(M, rows, d):
+    x = _n(_gen(rows + d), rows, d)
+    x8 = torch.empty(rows, d, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, device="cuda")
+    M.mla_quantize_i8(x, d, rows, d, x8, s)
+    want, scale = _codes64(x)
+    np.testing.assert_array_equal(x8.cpu().numpy(), want)
+    assert np.all(np.abs(s.double().cpu().numpy() - scale) <= F32 * scale)
+
+
 # ---- norms and residual -----------------------------------------------------
 
 NORMS = [  # n_tok, d, w_post, gate, residual, stride padding of u

@@ -227,3 +227,83 @@ def test_streams_and_graphs(M, impl):
     assert a.status() == 0 and b.status() == 0
     a.check()
     b.check()
+
+
+MANY_TOKENS = [  # units of many whole tokens, whose last keys only some of their rows see; unit counts past one block's scan
+    (1, 100, 2, [100, 150, 228]),
+    (2, 70, 3, [70, 71, 133, 200]),
+    (24, 9, 6, [9, 70, 64]),
+    (48, 4, 21, [4, 66, 130]),
+    (65, 3, 5, [3, 190]),
+    (128, 2, 3, [2, 3, 65, 70] * 300),
+    (16, 1, 40, [1, 2, 66] * 800),
+]
+
+
+@pytest.mark.parametrize("case", MANY_TOKENS)
+def test_units_of_many_tokens_and_many_units(M, case):
+    n_h, T_q, n_shared, own = case
+    c = Case(M, n_h, *V2, T_q, n_shared, own, M.IMPL_AUTO)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("impl", [0, 1])
+@pytest.mark.parametrize("n_h,T_q,own", [(16, 4, [4, 66, 131, 259]), (1, 70, [70, 130, 200]), (128, 3, [3, 66, 257]), (40, 3, [64])])
+def test_non_finite_keys_of_later_tokens(M, impl, n_h, T_q, own):
+    """Infinities and NaN in the rows that only a step's last tokens see leave the tokens before them as they are."""
+    c = Case(M, n_h, *V2, T_q, 3, own, impl)
+    hide = max(1, T_q // 2)                    # the last `hide` tokens of each sequence
+    for b, k in enumerate(own):
+        for j in range(k - hide, k):
+            page = int(c.table[b, (64 * 3 + j) // 64])
+            c.pool[page, j % 64, ::3] = float("nan")
+            c.pool[page, j % 64, 1::3] = float("inf")
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    got, lse = c.latent[:c.B * T_q].view(c.B, T_q, n_h, -1), c.lse[:c.B * T_q].view(c.B, T_q, n_h)
+    clean = Case(M, n_h, *V2, T_q, 3, own, impl)
+    clean.run()
+    torch.cuda.synchronize()
+    clean.check()
+    first = slice(0, T_q - hide)
+    assert torch.equal(got[:, first], clean.latent[:c.B * T_q].view(c.B, T_q, n_h, -1)[:, first])
+    assert torch.equal(lse[:, first], clean.lse[:c.B * T_q].view(c.B, T_q, n_h)[:, first])
+
+
+@pytest.mark.parametrize("n_h,T_q,n_shared,own", [(128, 1, 24, [70, 700, 300]), (128, 2, 70, [900, 1500]), (16, 2, 40, [70, 900, 500] * 4)])
+def test_growing_maxima(M, n_h, T_q, n_shared, own):
+    """Keys that grow along the sequence, so that the running maximum is passed by far again and again."""
+    c = Case(M, n_h, *V2, T_q, n_shared, own, 0)
+    P = 64 * n_shared
+    ramp = lambda pos: 0.25 + 6.0 * (pos / (P + max(own)))  # noqa: E731
+    for j in range(n_shared):
+        c.pool[c.shared[j].long()] *= ramp(64 * j)
+    for b, k in enumerate(own):
+        for j in range((k + 63) // 64):
+            c.pool[c.table[b, n_shared + j].long()] *= ramp(P + 64 * j)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    prefix = c.pool[c.shared.long()].reshape(-1, 576)
+    scale = 1.0 / math.sqrt(192)
+    for b, k in enumerate(own):
+        ids = c.table[b, n_shared:(P + k + 63) // 64].long()
+        keys = torch.cat([prefix, c.pool[ids].reshape(-1, 576)[:k]]).double()
+        for t in range(T_q):
+            n = b * T_q + t
+            see = keys[:P + k - T_q + t + 1]
+            q = torch.cat([c.q_abs[n], c.q_r[n]], 1).double()
+            s = q @ see.T * scale
+            want = torch.logsumexp(s, 1)
+            p = torch.exp(s - want[:, None])
+            o, mag = p @ see[:, :512], p @ see[:, :512].abs()
+            # a float32 sum of 576 products is off by at most 576 2^-24 of their magnitudes, and a weight (and
+            # the lse) by as much again through the scaled score and its exponent
+            err = (577 * 2.0 ** -24 * (q.abs() @ see.abs().T) * scale + 2.0 ** -22 * s.abs()).amax(1)
+            got, lse = c.latent[n].double(), c.lse[n].double()
+            assert ((got - o).abs() <= (BF + 2 * err[:, None] + SCORE) * mag + BF * o.abs()).all(), (b, t)
+            assert ((lse - want).abs() <= err + SCORE).all(), (b, t)
