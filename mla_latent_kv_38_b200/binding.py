@@ -128,9 +128,11 @@ def _current_stream():
 
 # torch's own query of the current stream's handle, where this torch has it: the
 # Stream object costs 3.3 us a call, more than the launch
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+    _raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
     def _current_stream():  # noqa: F811
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_raw_device())
 
 
 def _stream(stream):
@@ -299,42 +301,44 @@ def mla_decode_shared_workspace_bytes(cfg: MlaConfig, B: int, T_q: int, max_spli
     return int(_lib.mla_decode_shared_workspace_bytes(ctypes.byref(cfg), int(B), int(T_q), int(max_splits)))
 
 
+# The layer operators run for microseconds: ctypes converts their numbers itself.
+
 def mla_decode_shared(cfg: MlaConfig, q_abs, q_r, pool, num_blocks: int, shared_table, n_shared: int, block_table,
                       max_blocks_per_seq: int, seq_lens, B: int, T_q: int, max_splits: int,
                       workspace, ws_bytes: int, out_latent, out_lse, stream=None):
     """mla_decode of a batch whose sequences share their first n_shared cache pages."""
     _check("mla_decode_shared", _lib.mla_decode_shared(
-        ctypes.byref(cfg), _ptr(q_abs), _ptr(q_r), _ptr(pool), int(num_blocks), _ptr(shared_table), int(n_shared),
-        _ptr(block_table), int(max_blocks_per_seq), _ptr(seq_lens), int(B), int(T_q), int(max_splits), _ptr(workspace),
-        int(ws_bytes), _ptr(out_latent), _ptr(out_lse), _stream(stream)))
+        ctypes.byref(cfg), _ptr(q_abs), _ptr(q_r), _ptr(pool), num_blocks, _ptr(shared_table), n_shared,
+        _ptr(block_table), max_blocks_per_seq, _ptr(seq_lens), B, T_q, max_splits, _ptr(workspace),
+        ws_bytes, _ptr(out_latent), _ptr(out_lse), _stream(stream)))
 
 
 def mla_quantize_i8(x, ld_x: int, n_rows: int, d: int, x8, scale, stream=None):
     """Rows of a bf16 matrix (ld_x elements apart) as int8 codes with a float32 scale each."""
-    _check("mla_quantize_i8", _lib.mla_quantize_i8(_ptr(x), int(ld_x), int(n_rows), int(d), _ptr(x8), _ptr(scale),
+    _check("mla_quantize_i8", _lib.mla_quantize_i8(_ptr(x), ld_x, n_rows, d, _ptr(x8), _ptr(scale),
                                                    _stream(stream)))
 
 
 def mla_linear_i8(x8, ld_x: int, x_scale, w8, w_scale, out, n_tok: int, d_in: int, d_out: int, dev_status=None,
                   stream=None):
     """out = (x8 w8^T) x_scale w_scale in bf16: an int8 projection with scales per token and output channel."""
-    _check("mla_linear_i8", _lib.mla_linear_i8(_ptr(x8), int(ld_x), _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(out),
-                                               int(n_tok), int(d_in), int(d_out), _ptr(dev_status), _stream(stream)))
+    _check("mla_linear_i8", _lib.mla_linear_i8(_ptr(x8), ld_x, _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(out),
+                                               n_tok, d_in, d_out, _ptr(dev_status), _stream(stream)))
 
 
 def mla_block_norm(u, ld_u: int, w_post, gate, ld_gate: int, alpha: float, residual, residual_out, w_pre, eps: float,
                    n_tok: int, d: int, out=None, out8=None, out8_scale=None, stream=None):
     """Block output normed, gated, scaled and added to the residual, and the next block's norm (bf16 and / or int8)."""
     _check("mla_block_norm", _lib.mla_block_norm(
-        _ptr(u), int(ld_u), _ptr(w_post), _ptr(gate), int(ld_gate), float(alpha), _ptr(residual), _ptr(residual_out),
-        _ptr(w_pre), float(eps), int(n_tok), int(d), _ptr(out), _ptr(out8), _ptr(out8_scale), _stream(stream)))
+        _ptr(u), ld_u, _ptr(w_post), _ptr(gate), ld_gate, alpha, _ptr(residual), _ptr(residual_out),
+        _ptr(w_pre), eps, n_tok, d, _ptr(out), _ptr(out8), _ptr(out8_scale), _stream(stream)))
 
 
 def _norm_rope_append(name, cfg, q, kv, ld_kv, w_kv, eps, positions, rope_table, max_pos, block_table,
                       max_blocks_per_seq, pool, num_blocks, B, T_q, q_c, q_r, dev_status, stream):
     _check(name, getattr(_lib, name)(
-        ctypes.byref(cfg), _ptr(q), _ptr(kv), int(ld_kv), _ptr(w_kv), float(eps), _ptr(positions), _ptr(rope_table),
-        int(max_pos), _ptr(block_table), int(max_blocks_per_seq), _ptr(pool), int(num_blocks), int(B), int(T_q),
+        ctypes.byref(cfg), _ptr(q), _ptr(kv), ld_kv, _ptr(w_kv), eps, _ptr(positions), _ptr(rope_table),
+        max_pos, _ptr(block_table), max_blocks_per_seq, _ptr(pool), num_blocks, B, T_q,
         _ptr(q_c), _ptr(q_r), _ptr(dev_status), _stream(stream)))
 
 

@@ -199,10 +199,13 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
         const int j = e >> 5, o = o0 + 4 * (e & 31);
         if (o >= p.d_out) continue;
         int4 sum = make_int4(0, 0, 0, 0);
-        for (int q = 0; q < parts; ++q) {
-            const int4 v = ptx::ld_cluster_int4(ptx::map_to_rank(sbase + 16u * static_cast<uint32_t>(e), q));
-            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        }
+        int4 v[kMaxCluster];   // all parts requested together
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+            if (q < parts) v[q] = ptx::ld_cluster_int4(ptx::map_to_rank(sbase + 16u * static_cast<uint32_t>(e), q));
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+            if (q < parts) sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
         const float sx = p.x_scale[n0 + j];
         const float* sw = p.w_scale + o;
         *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(n0 + j) * p.d_out + o) =

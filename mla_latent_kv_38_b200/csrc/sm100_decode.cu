@@ -1328,10 +1328,13 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um
     }
 }
 
-// LSE merge of the partial slots of every unit covered by more than one
-// cluster: one warp per (unit, head row), a lane per 16 latent columns.  The
-// slots of unit u are meta.y + u .. meta.y + u + meta.z - 1.  Units of an
-// invalid sequence (kv_len 0) get zeros and lse = -inf.
+// LSE merge of the partial slots: a warp per query row, a lane per 4 x 4 latent
+// columns (16-byte loads and 8-byte stores of consecutive lanes).  mla_decode:
+// rows of units covered by one cluster were written by the decode kernel; the
+// others' partials are the slots meta.y + u .. meta.y + u + meta.z - 1 of unit
+// u.  Shared decode with prefix units: every row, from its prefix unit's slots
+// and its sequence unit's.  Rows of an invalid sequence (kv_len 0) get zeros
+// and lse = -inf.
 //
 // The partial rows were written by the decode kernel just before and are read
 // from L2 (ld.global.cg).  The first two slots' rows are fetched together with
@@ -1340,133 +1343,68 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um
 // Blocks of 8 warps, at most 64 registers a thread: 4 blocks per SM, one wave
 // for the 4,096 rows of 32 split units.  (Blocks of 4 warps doubled the merge
 // at prefill sizes, where most of the U x 128 rows belong to whole units and
-// the time goes into scheduling blocks that exit at once.)
-__global__ void __launch_bounds__(256, 4)
+// the time goes into scheduling blocks that exit at once; one wave of blocks
+// that walk the rows was no faster.)
+template <bool kShared>
+__global__ void __launch_bounds__(256, kShared ? 3 : 4)
 mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restrict__ part_o,
                        const float* __restrict__ part_lse, uint16_t* __restrict__ out_latent,
-                       float* __restrict__ out_lse, int n_h, int n_hb, int B, int T_q, int U) {
+                       float* __restrict__ out_lse, const UnitMap um, int rows) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int wg = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int u = wg >> 7, row = wg & 127;
-    if (u >= U) return;
-    const int4 meta = unit_meta[u];
-    auto out_row = [&]() {   // this warp's output row
-        const UnitIdx x = unit_index(u, n_hb, B);
-        return static_cast<size_t>(x.b * T_q + x.t) * n_h + x.hb * 128 + row;
+    // row r: its sequence unit (counted behind the prefix units), its row in
+    // the unit, and the output row
+    struct Place {
+        int uo, unit_row, out;
     };
-    if (meta.x == 0) {
-        const size_t grow = out_row();
-        uint4* dst = reinterpret_cast<uint4*>(out_latent + grow * kDc + lane * 16);
-        dst[0] = make_uint4(0, 0, 0, 0);
-        dst[1] = make_uint4(0, 0, 0, 0);
-        if (lane == 0) out_lse[grow] = -INFINITY;
-        return;
-    }
-    const int parts = meta.z;   // <= kClusters
-    if (parts <= 1) return;
-    const size_t slot0 = static_cast<size_t>(meta.y) + u;
-    const float* lse_row = part_lse + slot0 * 128 + row;                                       // slot i at + 128 i
-    const float4* o_row = reinterpret_cast<const float4*>(part_o + (slot0 * 128 + row) * kDc) + lane * 4;
-    constexpr size_t kSlot4 = static_cast<size_t>(128) * kDc / 4;                             // float4 per slot
-    auto load_pair = [&](float4 (&v)[2][4], int i) {   // slots i, i + 1 (zeros past the last)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[0][k] = __ldcg(o_row + i * kSlot4 + k);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            v[1][k] = i + 1 < parts ? __ldcg(o_row + (i + 1) * kSlot4 + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    float4 v[2][4];
-    load_pair(v, 0);
-    // log-sum-exp of slot lane + 32 k in ls[k] (parts <= 74 < 96)
-    float ls[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) ls[k] = lane + 32 * k < parts ? __ldcg(lse_row + 128 * (lane + 32 * k)) : -INFINITY;
-    const float mx = warp_max(fmaxf(fmaxf(ls[0], ls[1]), ls[2]));
-    auto w_of = [&](float l) { return l == -INFINITY ? 0.f : ex2((l - mx) * kLog2e); };
-    const float z = warp_sum(w_of(ls[0]) + w_of(ls[1]) + w_of(ls[2]));
-    auto weight = [&](int i) {   // slot i's weight, from the lane that holds its log-sum-exp
-        const float l = i < 32 ? ls[0] : (i < 64 ? ls[1] : ls[2]);
-        return w_of(__shfl_sync(0xffffffffu, l, i & 31));
-    };
-    float acc[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    for (int i = 0; i < parts; i += 2) {
-        if (i > 0) load_pair(v, i);
-        const float w0 = weight(i), w1 = i + 1 < parts ? weight(i + 1) : 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            acc[4 * k + 0] = fmaf(w1, v[1][k].x, fmaf(w0, v[0][k].x, acc[4 * k + 0]));
-            acc[4 * k + 1] = fmaf(w1, v[1][k].y, fmaf(w0, v[0][k].y, acc[4 * k + 1]));
-            acc[4 * k + 2] = fmaf(w1, v[1][k].z, fmaf(w0, v[0][k].z, acc[4 * k + 2]));
-            acc[4 * k + 3] = fmaf(w1, v[1][k].w, fmaf(w0, v[0][k].w, acc[4 * k + 3]));
+    auto place = [&](int r) {
+        if constexpr (kShared) {
+            const int n = r / um.n_h, head = r - n * um.n_h;
+            const int b = n / um.T_q, t = n - b * um.T_q;
+            const int group = t / um.tok_per_unit;
+            const bool many = um.tok_per_unit > 1;
+            return Place{(group * um.B + b) * um.n_hb + (many ? 0 : head >> 7),
+                         many ? (t - group * um.tok_per_unit) * um.n_h + head : head & 127, r};
+        } else {
+            const UnitIdx k = unit_index(r >> 7, um.n_hb, um.B);
+            return Place{r >> 7, r & 127, (k.b * um.T_q + k.t) * um.n_h + k.hb * 128 + (r & 127)};
         }
-    }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
-    uint32_t pk[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    const size_t grow = out_row();
-    uint4* dst = reinterpret_cast<uint4*>(out_latent + grow * kDc + lane * 16);
-    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    if (lane == 0) out_lse[grow] = z > 0.f ? mx + logf(z) : -INFINITY;
-}
-
-// The same for the shared decode: one warp per query row.  With prefix units
-// the row's partials are those of its prefix unit and of its sequence unit;
-// otherwise only units cut between clusters left partials.
-__global__ void __launch_bounds__(256, 3)
-mla_sm100_merge_shared_kernel(const int4* __restrict__ unit_meta, const float* __restrict__ part_o,
-                              const float* __restrict__ part_lse, uint16_t* __restrict__ out_latent,
-                              float* __restrict__ out_lse, const UnitMap um) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int grow = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (grow >= um.n_rows) return;
-    const int n = grow / um.n_h, head = grow - n * um.n_h;
-    const int b = n / um.T_q, t = n - b * um.T_q;
-    const int group = t / um.tok_per_unit;
-    const int hb = um.tok_per_unit > 1 ? 0 : head >> 7;
-    const int unit_row = um.tok_per_unit > 1 ? (t - group * um.tok_per_unit) * um.n_h + head : head & 127;
-    const int uo = (group * um.B + b) * um.n_hb + hb;
-    const int4 own = unit_meta[um.n_prefix + uo];
-    uint4* dst = reinterpret_cast<uint4*>(out_latent + static_cast<size_t>(grow) * kDc + lane * 16);
+    };
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const Place at = place(r);
+    const int4 own = unit_meta[um.n_prefix + at.uo];
+    int4 pre = make_int4(0, 0, 0, 0);
+    if (kShared && um.n_prefix > 0) pre = unit_meta[r >> 7];
+    uint2* dst = reinterpret_cast<uint2*>(out_latent + static_cast<size_t>(at.out) * kDc) + lane;
     if (own.x == 0) {   // the sequence's length is out of range
-        dst[0] = make_uint4(0, 0, 0, 0);
-        dst[1] = make_uint4(0, 0, 0, 0);
-        if (lane == 0) out_lse[grow] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint2(0, 0);
+        if (lane == 0) out_lse[at.out] = -INFINITY;
         return;
     }
-    int n_pre = 0;   // partials of the prefix unit
-    size_t pre_row = 0;
-    if (um.n_prefix > 0) {
-        const int4 pre = unit_meta[grow >> 7];
-        n_pre = pre.z;
-        pre_row = (static_cast<size_t>(pre.y) + (grow >> 7)) * 128 + (grow & 127);
-    } else if (own.z <= 1) {
-        return;   // written by the decode kernel
-    }
-    const size_t own_row = own_slot_row(own.y, uo, um) + unit_row;
-    const int parts = n_pre + own.z;   // <= 2 kClusters
+    const int n_pre = pre.z;
+    if (n_pre == 0 && own.z <= 1) return;   // written by the decode kernel
+    const int parts = n_pre + own.z;          // <= 2 kClusters
+    const size_t pre_row = (static_cast<size_t>(pre.y) + (r >> 7)) * 128 + (r & 127);
+    const size_t own_row = (kShared ? own_slot_row(own.y, at.uo, um)
+                                    : (static_cast<size_t>(own.y) + at.uo) * 128) + at.unit_row;
+    const size_t own_step = kShared ? um.own_rows : 128;
     auto row_of = [&](int i) {
-        return i < n_pre ? pre_row + static_cast<size_t>(i) * 128
-                         : own_row + static_cast<size_t>(i - n_pre) * um.own_rows;
+        return kShared && i < n_pre ? pre_row + static_cast<size_t>(i) * 128 : own_row + (i - n_pre) * own_step;
     };
     auto load_pair = [&](float4 (&v)[2][4], int i) {   // partials i, i + 1 (zeros past the last)
-        const float4* a = reinterpret_cast<const float4*>(part_o + row_of(i) * kDc) + lane * 4;
-        const float4* c = reinterpret_cast<const float4*>(part_o + row_of(min(i + 1, parts - 1)) * kDc) + lane * 4;
+        const float4* a = reinterpret_cast<const float4*>(part_o + row_of(i) * kDc) + lane;
+        const float4* c = reinterpret_cast<const float4*>(part_o + row_of(min(i + 1, parts - 1)) * kDc) + lane;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[0][k] = __ldcg(a + k);
+        for (int k = 0; k < 4; ++k) v[0][k] = __ldcg(a + 32 * k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[1][k] = i + 1 < parts ? __ldcg(c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 4; ++k) v[1][k] = i + 1 < parts ? __ldcg(c + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     float4 v[2][4];
     load_pair(v, 0);
-    constexpr int kPer = (2 * kClusters + 31) / 32;   // partial lane + 32 k in ls[k]
+    constexpr int kPer = ((kShared ? 2 : 1) * kClusters + 31) / 32;   // log-sum-exp of partial lane + 32 k
     float ls[kPer];
     float mx = -INFINITY;
 #pragma unroll
@@ -1480,7 +1418,7 @@ mla_sm100_merge_shared_kernel(const int4* __restrict__ unit_meta, const float* _
 #pragma unroll
     for (int k = 0; k < kPer; ++k) z += w_of(ls[k]);
     z = warp_sum(z);
-    auto weight = [&](int i) {
+    auto weight = [&](int i) {   // partial i's weight, from the lane that holds its log-sum-exp
         float l = ls[0];
 #pragma unroll
         for (int k = 1; k < kPer; ++k) l = (i >> 5) == k ? ls[k] : l;
@@ -1492,22 +1430,27 @@ mla_sm100_merge_shared_kernel(const int4* __restrict__ unit_meta, const float* _
     for (int i = 0; i < parts; i += 2) {
         if (i > 0) load_pair(v, i);
         const float w0 = weight(i), w1 = i + 1 < parts ? weight(i + 1) : 0.f;
+        if (kShared) {   // a partial of weight zero holds nothing that the row sees
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (w0 == 0.f) v[0][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (w1 == 0.f) v[1][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            // a partial of weight zero holds nothing that the row sees
-            acc[4 * k + 0] += (w0 != 0.f ? w0 * v[0][k].x : 0.f) + (w1 != 0.f ? w1 * v[1][k].x : 0.f);
-            acc[4 * k + 1] += (w0 != 0.f ? w0 * v[0][k].y : 0.f) + (w1 != 0.f ? w1 * v[1][k].y : 0.f);
-            acc[4 * k + 2] += (w0 != 0.f ? w0 * v[0][k].z : 0.f) + (w1 != 0.f ? w1 * v[1][k].z : 0.f);
-            acc[4 * k + 3] += (w0 != 0.f ? w0 * v[0][k].w : 0.f) + (w1 != 0.f ? w1 * v[1][k].w : 0.f);
+            acc[4 * k + 0] = fmaf(w1, v[1][k].x, fmaf(w0, v[0][k].x, acc[4 * k + 0]));
+            acc[4 * k + 1] = fmaf(w1, v[1][k].y, fmaf(w0, v[0][k].y, acc[4 * k + 1]));
+            acc[4 * k + 2] = fmaf(w1, v[1][k].z, fmaf(w0, v[0][k].z, acc[4 * k + 2]));
+            acc[4 * k + 3] = fmaf(w1, v[1][k].w, fmaf(w0, v[0][k].w, acc[4 * k + 3]));
         }
     }
     const float inv = z > 0.f ? 1.f / z : 0.f;
-    uint32_t pk[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    if (lane == 0) out_lse[grow] = z > 0.f ? mx + logf(z) : -INFINITY;
+    for (int k = 0; k < 4; ++k)
+        dst[32 * k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                                 pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    if (lane == 0) out_lse[at.out] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1668,14 +1611,10 @@ cudaError_t launch_units(const DecodeParams& P, const UnitMap& um, int U, size_t
     if (e != cudaSuccess) return e;
     e = launch_pdl(mla_decode_sm100_kernel<kShared>, dim3(2 * kClusters), dim3(kThreads), kSmemBytes, stream, k);
     if (e != cudaSuccess) return e;
-    if constexpr (kShared)
-        return launch_pdl(mla_sm100_merge_shared_kernel, dim3((um.n_rows + 7) / 8), dim3(256), 0, stream,
-                          static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),
-                          static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, um);
-    const int rows = U * 128;
-    return launch_pdl(mla_sm100_merge_kernel, dim3((rows + 7) / 8), dim3(256), 0, stream,
+    const int rows = kShared ? um.n_rows : U * 128;
+    return launch_pdl(mla_sm100_merge_kernel<kShared>, dim3((rows + 7) / 8), dim3(256), 0, stream,
                       static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),
-                      static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, P.n_h, um.n_hb, P.B, P.T_q, U);
+                      static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, um, rows);
 }
 
 }  // namespace

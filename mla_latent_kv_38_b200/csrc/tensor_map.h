@@ -60,10 +60,13 @@ inline bool encode_tiled_cached(CUtensorMap* m, CUtensorMapDataType dtype, uint3
     k.dtype = static_cast<uint32_t>(dtype);
     k.rank = rank;
     k.swizzle = static_cast<uint32_t>(swizzle);
-    uint64_t h = 1469598103934665603ull;   // FNV-1a over the key bytes
-    const unsigned char* kb = reinterpret_cast<const unsigned char*>(&k);
-    for (size_t i = 0; i < sizeof(k); ++i) h = (h ^ kb[i]) * 1099511628211ull;
-    Slot& sl = slots[h % kSlots];
+    // FNV-1a over the key's 8-byte words, its high bits folded into the low ones
+    uint64_t h = 1469598103934665603ull;
+    uint64_t words[(sizeof(k) + 7) / 8] = {};
+    memcpy(words, &k, sizeof(k));
+    for (uint64_t w : words) h = (h ^ w) * 1099511628211ull;
+    h ^= h >> 32;
+    Slot& sl = slots[(h ^ (h >> 16)) % kSlots];
     {
         std::lock_guard<std::mutex> lock(mu);
         if (sl.valid && memcmp(&sl.key, &k, sizeof(k)) == 0) {
