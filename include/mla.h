@@ -392,12 +392,17 @@ int mla_decode_e4m3(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf
  *     64 * n_shared + T_q <= seq_lens[b] <= 64 * max_blocks_per_seq.  A
  *     sequence that breaks this sets MLA_STATUS_BAD_SEQ_LEN; its outputs are
  *     zero and -inf.
- * The shared and the own keys of a row are scored in separate units of work
- * and always merged by the log-sum-exp reduction.  tcgen05 kernels (cfg->impl
- * 0 or 2): d_c = 512, d_r = 64 and any n_h -- the query rows of the batch are
- * taken 128 at a time against the shared keys, whatever their heads.  Portable
- * kernels: every supported shape.  max_splits as for mla_decode, for each of
- * the two key ranges. */
+ * A key that only a step's later tokens see does not reach the tokens before
+ * them, whatever it holds.
+ * tcgen05 kernels (cfg->impl 0 or 2): d_c = 512, d_r = 64 and any n_h, with
+ * B * T_q * ceil(n_h / 128) * max_blocks_per_seq < 2^29 (MLA_ERR_SIZE beyond).
+ * They work on units of up to 128 query rows.  A unit of whole tokens of one
+ * sequence walks the shared pages and its own; where such units would leave too
+ * many of the 128 rows empty, the shared pages are walked by units of 128
+ * consecutive rows of the batch, whatever their sequence, and the results of
+ * the two key ranges joined by their log-sum-exps.  Portable kernels: every
+ * supported shape, the two ranges always apart.  max_splits as for mla_decode,
+ * for each walk. */
 int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf16* q_r,
                       const mla_bf16* pool, int num_blocks, const int32_t* shared_table, int n_shared,
                       const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,

@@ -35,10 +35,16 @@
 //  * Warp roles per CTA: warp 0 S producer, warp 1 tensor-memory allocation
 //    and (CTA 0) the S MMAs, warp 2 (CTA 0) the P.V MMAs, warp 3 V producer,
 //    warps 4-11 softmax and epilogue (two warps per tensor-memory lane
-//    quadrant).  S is double
-//    buffered; P is written to shared memory in two key halves, each released
+//    quadrant).  S is double buffered and free again once its scores are in
+//    registers; P is written to shared memory in two key halves, each released
 //    as soon as its MMAs complete.  The running max is rescaled lazily (only
 //    when it grows by 2^8).
+//  * What bounds it with the cache in L2 (64 x 4 tokens of 128 heads behind 8,192
+//    shared keys, 490 us): the loads.  A tile takes 344 KB per SM at 12.4 TB/s
+//    over all SMs, which is what TMA boxes of this shape reach with 192 KB in
+//    flight per SM; its MMAs need two thirds of that time.  Keeping the query in
+//    shared memory takes 72 KB off each tile and as much off the rings: 480 us
+//    there, 110 instead of 108 us for a shard's batch of short units.
 //  * Work: the tiles of all (sequence, token, head block) units are laid end
 //    to end and cut into contiguous ranges, one per cluster (persistent, 74
 //    clusters on 148 SMs).  Each CTA computes the cut from the sequence
@@ -234,7 +240,7 @@ __device__ __forceinline__ int unit_keys(const int32_t* seq_lens, int u, const U
         if (u < um.n_prefix) return own0;
         const UnitIdx x = unit_index(u - um.n_prefix, um.n_hb, um.B);
         const int L = seq_lens[x.b];
-        if (L - own0 < um.T_q || L > um.max_blocks * kPage) return 0;
+        if (L < um.T_q + own0 || L > um.max_blocks * kPage) return 0;
         return L - um.T_q + min(um.T_q, (x.t + 1) * um.tok_per_unit) - (um.n_prefix > 0 ? own0 : 0);
     } else {
         const UnitIdx x = unit_index(u, um.n_hb, um.B);

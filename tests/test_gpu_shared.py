@@ -170,6 +170,16 @@ def test_invalid_lengths_are_flagged_and_leave_the_others(M, impl):
 
 
 @pytest.mark.parametrize("impl", [0, 1])
+def test_lengths_at_the_ends_of_int32(M, impl):
+    c = Case(M, 16, *V2, 1, 3, [0, 70, 0, 130], impl)
+    c.lens[0], c.lens[2] = -2 ** 31, 2 ** 31 - 1
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == M.MLA_STATUS_BAD_SEQ_LEN
+    c.check()
+
+
+@pytest.mark.parametrize("impl", [0, 1])
 def test_bad_blocks_are_flagged(M, impl):
     """Entries outside the pool, shared and own, are flagged; nothing is read out of bounds."""
     for where in ("shared", "own"):

@@ -44,6 +44,8 @@ def test_decode_shared_refusals(M):
     for bad in (dict(B=0), dict(T_q=0), dict(B=65536), dict(num_blocks=0), dict(mbps=0), dict(splits=-1),
                 dict(n_shared=-1), dict(n_shared=65), dict(mbps=(1 << 24) + 1)):
         assert call(**bad) == SIZE, bad
+    # pages of all units together are counted in 32 bits
+    assert call(mbps=1 << 24) == SIZE and call(c=_cfg(M, n_h=129), B=64, mbps=1 << 22) == SIZE
     assert call(ws=ctypes.c_void_p(FAKE + 16)) == WORKSPACE
     need = M.mla_decode_shared_workspace_bytes(_cfg(M), 32, 1, 0)
     assert need > 0 and need % 256 == 0
