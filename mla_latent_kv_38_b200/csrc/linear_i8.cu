@@ -70,7 +70,7 @@ __device__ __forceinline__ float scaled(int sum, float sx, float sw) { return st
 // split
 // ---------------------------------------------------------------------------
 
-constexpr int kSplitThreads = 128;
+constexpr int kSplitThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kSplitRing = 200 * 1024;       // one CTA per SM
 constexpr uint32_t kSplitRingHalf = 108 * 1024;   // two
@@ -182,35 +182,58 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
 
     // Partial sums to shared memory as [token][128 channels] (a warp writes 32
     // consecutive channels), then the cluster's CTAs share the outputs: each
-    // adds its vectors of four channels over all parts.
+    // adds its vectors of four channels over all parts.  A thread keeps its
+    // four channels, and takes kOutStep tokens at a time: one at a time, and
+    // with 128 threads, this took longer than the product of 256 tokens.
     int* part = reinterpret_cast<int*>(smem);
     const int valid = min(p.nt, p.n_tok - n0);
     ptx::tc_fence_after();
-    for (int j0 = 0; j0 < valid; j0 += 16) {
+    for (int j0 = 16 * (warp >> 2); j0 < valid; j0 += 32) {
         uint32_t r[16];
-        ptx::tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + j0, r);
+        ptx::tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0, r);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(j0 + j) * 128 + threadIdx.x] = static_cast<int>(r[j]);
+        for (int j = 0; j < 16; ++j) part[(j0 + j) * 128 + (threadIdx.x & 127)] = static_cast<int>(r[j]);
     }
+    const int c4 = 4 * lane, o = o0 + c4;
+    const bool in = o < p.d_out;
+    float sw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sw[k] = in ? p.w_scale[o + k] : 0.f;
     ptx::tc_fence_before();
     ptx::cluster_sync();
-    for (int e = rank * kSplitThreads + threadIdx.x; e < valid * 32; e += parts * kSplitThreads) {
-        const int j = e >> 5, o = o0 + 4 * (e & 31);
-        if (o >= p.d_out) continue;
-        int4 sum = make_int4(0, 0, 0, 0);
-        int4 v[kMaxCluster];   // all parts requested together
+    constexpr int kOutStep = 4, kWarps = kSplitThreads / 32;
+    const int stride = parts * kWarps;   // tokens between a warp's
+    for (int j = rank * kWarps + warp; j < valid; j += kOutStep * stride) {
+        int4 sum[kOutStep];
+        float sx[kOutStep];
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-            if (q < parts) v[q] = ptx::ld_cluster_int4(ptx::map_to_rank(sbase + 16u * static_cast<uint32_t>(e), q));
+        for (int u = 0; u < kOutStep; ++u) {
+            sum[u] = make_int4(0, 0, 0, 0);
+            sx[u] = j + u * stride < valid ? p.x_scale[n0 + j + u * stride] : 0.f;
+        }
+        for (int q = 0; q < parts; q += 2) {
+            int4 v[2][kOutStep];   // two parts of all the tokens requested together
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-            if (q < parts) sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
-        const float sx = p.x_scale[n0 + j];
-        const float* sw = p.w_scale + o;
-        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(n0 + j) * p.d_out + o) =
-            make_uint2(pack_bf16x2(scaled(sum.x, sx, sw[0]), scaled(sum.y, sx, sw[1])),
-                       pack_bf16x2(scaled(sum.z, sx, sw[2]), scaled(sum.w, sx, sw[3])));
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int u = 0; u < kOutStep; ++u)
+                    v[w][u] = q + w < parts && j + u * stride < valid
+                                  ? ptx::ld_cluster_int4(ptx::map_to_rank(
+                                        sbase + 512u * static_cast<uint32_t>(j + u * stride) + 16u * lane, q + w))
+                                  : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int u = 0; u < kOutStep; ++u)
+                    sum[u].x += v[w][u].x, sum[u].y += v[w][u].y, sum[u].z += v[w][u].z, sum[u].w += v[w][u].w;
+        }
+#pragma unroll
+        for (int u = 0; u < kOutStep; ++u)
+            if (in && j + u * stride < valid)
+                *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(n0 + j + u * stride) * p.d_out + o) =
+                    make_uint2(pack_bf16x2(scaled(sum[u].x, sx[u], sw[0]), scaled(sum[u].y, sx[u], sw[1])),
+                               pack_bf16x2(scaled(sum[u].z, sx[u], sw[2]), scaled(sum[u].w, sx[u], sw[3])));
     }
     ptx::cluster_sync();   // the other CTAs have read this one's sums
     ptx::tc_fence_after();
@@ -221,11 +244,11 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
 // wide
 // ---------------------------------------------------------------------------
 
-constexpr int kWideThreads = 192;                // loads, MMAs, 4 x epilogue
+constexpr int kWideThreads = 320;                // loads, MMAs, 8 x epilogue
 constexpr int kWideStages = 6;
 constexpr uint32_t kWideStage = 2 * kOpBytes;    // this CTA's 128 tokens and 128 channels
-constexpr uint32_t kOffStage = kWideStages * kWideStage;       // epilogue staging: 2 x 4 KB per warp
-constexpr uint32_t kOffScales = kOffStage + 4 * 2 * 4096;      // the tile's 256 channel scales
+constexpr uint32_t kOffStage = kWideStages * kWideStage;       // epilogue staging: 4 KB per warp
+constexpr uint32_t kOffScales = kOffStage + 8 * 4096;      // the tile's 256 channel scales
 constexpr uint32_t kOffWideBars = kOffScales + 1024;
 enum { W_FULL = 0, W_EMPTY = W_FULL + kWideStages, W_ACC_FULL = W_EMPTY + kWideStages, W_ACC_FREE = W_ACC_FULL + 2,
        W_DRAIN = W_ACC_FREE + 2, W_BARS = W_DRAIN + 1 };
@@ -265,7 +288,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(bar(W_ACC_FULL + b), 1);   // each CTA: MMA commit
-            ptx::mbar_init(bar(W_ACC_FREE + b), 8);   // leader: 4 epilogue warps x 2 CTAs
+            ptx::mbar_init(bar(W_ACC_FREE + b), 16);  // leader: 8 epilogue warps x 2 CTAs
         }
         ptx::mbar_init(bar(W_DRAIN), 1);
         *abort_flag = 0;
@@ -346,36 +369,43 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             }
         }
     } else {
-        const int wq = warp & 3;   // tensor-memory lane quadrant
+        // two warps per tensor-memory lane quadrant, 128 of the 256 channels each
+        // (with one the epilogue, not the MMAs, set the pace: 63 us for 2,048
+        // tokens through 1,536 x 24,576)
+        const int wq = warp & 3, half = (warp - 2) >> 2;
         const int st = (warp - 2) * 32 + lane;
         float* scales = reinterpret_cast<float*>(smem + kOffScales);
-        unsigned char* stage = smem + kOffStage + (warp - 2) * 8192;
-        const uint32_t stage_u = sbase + kOffStage + (warp - 2) * 8192;
+        unsigned char* stage = smem + kOffStage + (warp - 2) * 4096;
+        const uint32_t stage_u = sbase + kOffStage + (warp - 2) * 4096;
         const int x7 = lane & 7;
-        int i = 0, stores = 0;
+        int i = 0;
         for (int t = cluster; t < p.tiles; t += clusters, ++i) {
             const int row0 = (t % p.m_tiles) * 256 + 128 * rank + 32 * wq, o0 = (t / p.m_tiles) * 256;
             const int b = i & 1;
-            ptx::named_bar_sync(1, 128);   // every warp has read the last tile's scales
-            for (int k = st; k < 256; k += 128) scales[k] = o0 + k < p.d_out ? p.w_scale[o0 + k] : 0.f;
+            ptx::named_bar_sync(1, 256);   // every warp has read the last tile's scales
+            scales[st] = o0 + st < p.d_out ? p.w_scale[o0 + st] : 0.f;
             const float sx = row0 + lane < p.n_tok ? p.x_scale[row0 + lane] : 0.f;
-            ptx::named_bar_sync(2, 128);
+            ptx::named_bar_sync(2, 256);
             bool ok = wait_bounded(bar(W_ACC_FULL + b), (i >> 1) & 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 2 * half; q < 2 * half + 2; ++q) {
                 if (!ok || row0 >= p.n_tok || o0 + 64 * q >= p.d_out) break;   // the same for the whole warp
                 uint32_t r[2][32];
                 const uint32_t src = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 256 * b + 64 * q;
                 ptx::tmem_ld32(src, r[0]);
                 ptx::tmem_ld32(src + 32, r[1]);
                 ptx::tmem_wait_ld();
-                // 32 rows x 64 bf16 in the store box's swizzled layout; two
-                // boxes per warp, so one store is read while the next is written
-                if (lane == 0) ptx::bulk_wait_read_but1();
+                if (q & 1) {   // the accumulator has been read: the MMAs may have it back
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+                }
+                // 32 rows x 64 bf16 in the store box's swizzled layout
+                if (lane == 0) ptx::bulk_wait_read_all();   // the last store has read its box
                 __syncwarp();
-                unsigned char* my_row = stage + (stores & 1) * 4096 + lane * 128;
+                unsigned char* my_row = stage + lane * 128;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float4 w0 = *reinterpret_cast<const float4*>(scales + 64 * q + 8 * k);
@@ -390,14 +420,16 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    ptx::tma_store_2d(&p.tm_out, stage_u + (stores & 1) * 4096, o0 + 64 * q, row0);
+                    ptx::tma_store_2d(&p.tm_out, stage_u, o0 + 64 * q, row0);
                     ptx::bulk_commit_group();
                 }
-                ++stores;
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+            // a warp that did not read its last columns hands the accumulator back here
+            if (!ok || row0 >= p.n_tok || o0 + 64 * (2 * half + 1) >= p.d_out) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+            }
         }
         if (lane == 0) ptx::bulk_wait_all();
     }
@@ -419,7 +451,12 @@ bool use_wide(int n_tok, int d_out) {
 cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
                          uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
     SplitArgs p;
-    const int tok_tiles = (n_tok + 255) / 256, o_tiles = (d_out + 127) / 128;
+    // Token tiles of 256, or of 128 or 64 where that leaves half the SMs without
+    // a tile (897 tokens through 272 x 464: 26.3 us with 256).
+    const int o_tiles = (d_out + 127) / 128;
+    int most_tok = 256;
+    while (most_tok > 64 && static_cast<long>(o_tiles) * ((n_tok + most_tok - 1) / most_tok) < kSms / 2) most_tok /= 2;
+    const int tok_tiles = (n_tok + most_tok - 1) / most_tok;
     p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
     p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
     // The largest cluster (a power of two: others leave SMs of a GPC unused)
