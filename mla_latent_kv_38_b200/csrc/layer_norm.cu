@@ -168,72 +168,91 @@ block_norm_kernel(const BlockNormArgs a) {
     }
 }
 
-// Codes and scale of a bf16 row: scale = max / 127, code = round(127 x / max).
-// 127 x is exact in float32 (8 + 7 bits), and the correctly rounded quotient
-// meets a half only where the exact one does, because a quotient of two 8-bit
-// mantissas times 254 that is no integer is at least 2^-17 of itself away from
-// one.  So the codes are those of exact arithmetic.  The division is taken only
-// where it matters: x (127 / max) is off by less than 127 x 2^-23 < 2e-5, so
-// its rounding stands unless it lies within 1e-4 of a half.
-// Bound by memory (3 bytes a value); the plain divisions alone took 40 us for
-// 2,048 rows of 16,384, their bytes 15.
-__device__ __forceinline__ uint2 quantize8(const uint4& w, float amax, float inv) {
+// Codes and scale of a bf16 row: scale = max / 127, code = round(127 x / max),
+// the codes those of exact arithmetic.  A quotient of two 8-bit mantissas times
+// 254 that is no integer is at least 2^-17 of itself away from one, so the
+// rounded fused product x (127 / max) is right but for quotients of exactly a
+// half.  Taken with a factor 2^-21 too small and one as much too large the two
+// differ there, and next to there: then the codes are divided for (127 x is
+// exact, and the correctly rounded quotient meets a half only where the exact
+// one does).  The kernel is bound by these instructions, not by its 3 bytes a
+// value: with a division each 40 us for 2,048 rows of 16,384, whose bytes take
+// 15.
+struct CodeFactor {
+    float amax, lo, hi;   // 127 / amax, 2^-21 of it below and above; 0 for a row of zeros
+};
+
+__device__ __forceinline__ CodeFactor code_factor(float amax) {
+    const float inv = amax > 0.f ? __fdiv_rn(127.f, amax) : 0.f;
+    return CodeFactor{amax, inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
+}
+
+__device__ __forceinline__ uint2 quantize8(const uint4& w, const CodeFactor& c) {
     float f[8], r[8];
     unpack8(w, f);
-    float far = 0.f;
+    uint32_t differ = c.hi > 3e38f ? 1u : 0u;   // (127 / amax overflows for the smallest rows)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float q = __fmul_rn(f[e], inv);
-        r[e] = __fadd_rn(q, kRound);
-        far = fmaxf(far, fabsf(q - __fsub_rn(r[e], kRound)));
+        r[e] = __fmaf_rn(f[e], c.lo, kRound);
+        differ |= __float_as_uint(r[e]) ^ __float_as_uint(__fmaf_rn(f[e], c.hi, kRound));
     }
-    if (far > 0.4999f || inv > 3e38f) {   // (127 / amax overflows for the smallest rows)
+    if (differ) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = __fadd_rn(amax > 0.f ? __fdiv_rn(127.f * f[e], amax) : 0.f, kRound);
+        for (int e = 0; e < 8; ++e)
+            r[e] = __fadd_rn(c.amax > 0.f ? __fdiv_rn(127.f * f[e], c.amax) : 0.f, kRound);
     }
     return pack_codes(r);
 }
 
-__device__ __forceinline__ float amax8(const uint4& w, float m) {
-    float f[8];
-    unpack8(w, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-    return m;
+// Largest magnitudes of eight values, two bf16 bit patterns at a time (the
+// patterns of positive values are in their order).
+__device__ __forceinline__ uint32_t amax8(const uint4& w, uint32_t m) {
+    const uint32_t a = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+    const uint32_t b = __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu);
+    return __vmaxu2(m, __vmaxu2(a, b));
+}
+__device__ __forceinline__ float amax_of(uint32_t m) {
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
 }
 
-// 127 / amax; zero for a row of zeros
-__device__ __forceinline__ float code_factor(float amax) { return amax > 0.f ? __fdiv_rn(127.f, amax) : 0.f; }
+// A block per row, rows with the grid's stride: kCachedRow vectors per thread
+// stay in registers between the maximum and the codes, and those of the block's
+// next row are requested in front of this row's maximum; the rest of a longer
+// row is read twice.
+constexpr int kCachedRow = 4;
 
-// kCached vectors of a row per thread stay in registers between the maximum and
-// the codes; longer rows are read again.  kWarpRow: a row per warp.
-template <int kCached, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 128 : 512, kWarpRow ? 4 : 2)
+__global__ void __launch_bounds__(512, 2)
 quantize_i8_kernel(const uint16_t* __restrict__ x, long ld_x, int n_rows, int d, int8_t* __restrict__ x8,
                    float* __restrict__ scale) {
     __shared__ float2 red[2][32];
     griddep_launch_dependents();
     griddep_wait();
     int turn = 0;
-    const int nv = d >> 3, T = kWarpRow ? 32 : blockDim.x, t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
-    const int per = kWarpRow ? blockDim.x >> 5 : 1;
-    for (long row = static_cast<long>(blockIdx.x) * per + (kWarpRow ? threadIdx.x >> 5 : 0); row < n_rows;
-         row += static_cast<long>(gridDim.x) * per) {
+    const int nv = d >> 3, T = blockDim.x, t = threadIdx.x;
+    uint4 v[kCachedRow], next[kCachedRow];
+    auto fetch = [&](long row) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + row * ld_x);
+#pragma unroll
+        for (int k = 0; k < kCachedRow; ++k) next[k] = t + k * T < nv ? src[t + k * T] : make_uint4(0, 0, 0, 0);
+    };
+    long row = blockIdx.x;
+    if (row < n_rows) fetch(row);
+    for (; row < n_rows; row += gridDim.x) {
+#pragma unroll
+        for (int k = 0; k < kCachedRow; ++k) v[k] = next[k];
+        if (row + gridDim.x < n_rows) fetch(row + gridDim.x);
         const uint4* src = reinterpret_cast<const uint4*>(x + row * ld_x);
         uint2* dst = reinterpret_cast<uint2*>(x8 + row * d);
-        uint4 v[kCached];
-        float m = 0.f;
+        uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kCached; ++k) v[k] = t + k * T < nv ? src[t + k * T] : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kCachedRow; ++k) m = amax8(v[k], m);
+        for (int j = t + kCachedRow * T; j < nv; j += T) m = amax8(src[j], m);
+        const float amax = row_reduce<false>(0.f, amax_of(m), red, turn).y;
+        const CodeFactor c = code_factor(amax);
 #pragma unroll
-        for (int k = 0; k < kCached; ++k) m = amax8(v[k], m);
-        for (int j = t + kCached * T; j < nv; j += T) m = amax8(src[j], m);
-        const float amax = row_reduce<kWarpRow>(0.f, m, red, turn).y;
-        const float inv = code_factor(amax);
-#pragma unroll
-        for (int k = 0; k < kCached; ++k)
-            if (t + k * T < nv) dst[t + k * T] = quantize8(v[k], amax, inv);
-        for (int j = t + kCached * T; j < nv; j += T) dst[j] = quantize8(src[j], amax, inv);
+        for (int k = 0; k < kCachedRow; ++k)
+            if (t + k * T < nv) dst[t + k * T] = quantize8(v[k], c);
+        for (int j = t + kCachedRow * T; j < nv; j += T) dst[j] = quantize8(src[j], c);
         if (t == 0) scale[row] = __fdiv_rn(amax, 127.f);
     }
 }
@@ -263,17 +282,14 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
 cudaError_t launch_quantize_i8(const uint16_t* x, long ld_x, int n_rows, int d, int8_t* x8, float* scale,
                                cudaStream_t stream) {
     const int nv = d / 8;
-    // many short rows: a warp each, all of a lane's vectors requested at once
-    // (2,048 rows of 1,536: 6.8 us with a block per row)
-    if (nv <= 256 && n_rows >= 4 * 148) {
-        const long blocks = (static_cast<long>(n_rows) + 3) / 4;
-        return launch_pdl(quantize_i8_kernel<8, true>, dim3(static_cast<unsigned>(blocks < 148 * 8 ? blocks : 148 * 8)),
-                          dim3(128), 0, stream, x, ld_x, n_rows, d, x8, scale);
-    }
-    const int threads = nv >= 512 ? 512 : (nv + 31) / 32 * 32;
-    const int most = 148 * 16;
-    return launch_pdl(quantize_i8_kernel<4, false>, dim3(n_rows < most ? n_rows : most), dim3(threads), 0, stream, x, ld_x,
-                      n_rows, d, x8, scale);
+    // as many threads as the row has vectors for few rows, kCachedRow vectors a
+    // thread for many, so that more rows are on their way per SM
+    const int want = n_rows <= 2 * 148 ? nv : (nv + kCachedRow - 1) / kCachedRow;
+    const int threads = want >= 512 ? 512 : (want + 31) / 32 * 32;
+    const int fit = 1024 / threads < 32 ? 1024 / threads : 32;   // resident blocks at 64 registers
+    const int most = 148 * fit;
+    return launch_pdl(quantize_i8_kernel, dim3(n_rows < most ? n_rows : most), dim3(threads), 0, stream, x, ld_x, n_rows,
+                      d, x8, scale);
 }
 
 }  // namespace mla

@@ -259,13 +259,30 @@ struct WideArgs {
     CUtensorMap tm_x;     // x8 [n_tok][d_in], boxes 128 x 128
     CUtensorMap tm_w;     // w8 [d_out][d_in], boxes 128 x 128
     CUtensorMap tm_out;   // out [n_tok][d_out] bf16, boxes 64 x 32 (stores)
+    CUtensorMap tm_w_cut; // w8, boxes 128 x (128 / cut)
     const float* x_scale;
     const float* w_scale;
     int32_t* status;
-    int n_tok, d_out, chunks, m_tiles, tiles;
+    int n_tok, d_out, chunks, m_tiles;
+    int whole;            // 256 x 256 tiles, in front of
+    int pieces;           // pieces of 256 / cut channels of the others
+    int cut;              // 1, 2 or 4
 };
 
-constexpr uint32_t kWideIdesc = ptx::idesc_i8_s32(256, 256);
+// The tiles of a cluster: t = cluster, cluster + clusters, .. < whole + pieces.
+// Tiles beyond whole rounds of all clusters are cut into pieces where these
+// still make one round: 768 tiles over 74 clusters end in 56 half tiles.
+struct WideTile {
+    int n0, o0, cols;   // first token and channel, channels
+};
+
+__device__ __forceinline__ WideTile wide_tile(const WideArgs& p, int t) {
+    const bool cut = t >= p.whole;
+    const int s = t - p.whole;
+    const int tile = cut ? p.whole + s / p.cut : t;
+    const int cols = cut ? 256 / p.cut : 256;
+    return WideTile{(tile % p.m_tiles) * 256, (tile / p.m_tiles) * 256 + (cut ? (s % p.cut) * cols : 0), cols};
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
@@ -313,8 +330,11 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
         // row: the clusters work on the same weights at the same time
         int e = 0;
         bool ok = true;
-        for (int t = cluster; t < p.tiles && ok; t += clusters) {
-            const int n0 = (t % p.m_tiles) * 256 + 128 * rank, o0 = (t / p.m_tiles) * 256 + 128 * rank;
+        for (int t = cluster; t < p.whole + p.pieces && ok; t += clusters) {
+            const WideTile w = wide_tile(p, t);
+            const int n0 = w.n0 + 128 * rank, o0 = w.o0 + w.cols / 2 * rank;
+            const void* tm_w = w.cols == 256 ? static_cast<const void*>(&p.tm_w) : &p.tm_w_cut;
+            const uint32_t tx = 2 * (kOpBytes + static_cast<uint32_t>(w.cols / 2) * kChunk);   // both CTAs'
             for (int c = 0; c < p.chunks; ++c, ++e) {
                 const int s = e % kWideStages;
                 bool good = true;
@@ -322,9 +342,9 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                     good = wait_bounded(bar(W_EMPTY + s), ((e / kWideStages) & 1) ^ 1, abort_flag, p.status);
                     if (good) {
                         const uint32_t st = sbase + s * kWideStage;
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(W_FULL + s), 2 * kWideStage);
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(W_FULL + s), tx);
                         ptx::tma_load_2d_pair_normal(st, &p.tm_x, static_cast<int>(kChunk) * c, n0, leader_bar(W_FULL + s));
-                        ptx::tma_load_2d_pair_normal(st + kOpBytes, &p.tm_w, static_cast<int>(kChunk) * c, o0,
+                        ptx::tma_load_2d_pair_normal(st + kOpBytes, tm_w, static_cast<int>(kChunk) * c, o0,
                                                      leader_bar(W_FULL + s));
                     }
                 }
@@ -335,8 +355,9 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
         if (rank == 0) {
             int e = 0, i = 0;
             bool ok = true;
-            for (int t = cluster; t < p.tiles && ok; t += clusters, ++i) {
+            for (int t = cluster; t < p.whole + p.pieces && ok; t += clusters, ++i) {
                 const int b = i & 1;
+                const uint32_t idesc = ptx::idesc_i8_s32(256, wide_tile(p, t).cols);
                 ok = __all_sync(0xffffffffu, wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status));
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -351,7 +372,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                                        w = ptx::smem_desc_sw128(st + kOpBytes, 16, 1024);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_pair_i8_ss(tmem + 256 * b, a + ((32 * kk) >> 4), w + ((32 * kk) >> 4), kWideIdesc,
+                            ptx::mma_pair_i8_ss(tmem + 256 * b, a + ((32 * kk) >> 4), w + ((32 * kk) >> 4), idesc,
                                                 (c | kk) ? 1u : 0u);
                         ptx::mma_commit_pair(bar(W_EMPTY + s), 0x3);
                         if (c == p.chunks - 1) ptx::mma_commit_pair(bar(W_ACC_FULL + b), 0x3);
@@ -379,8 +400,12 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
         const uint32_t stage_u = sbase + kOffStage + (warp - 2) * 4096;
         const int x7 = lane & 7;
         int i = 0;
-        for (int t = cluster; t < p.tiles; t += clusters, ++i) {
-            const int row0 = (t % p.m_tiles) * 256 + 128 * rank + 32 * wq, o0 = (t / p.m_tiles) * 256;
+        for (int t = cluster; t < p.whole + p.pieces; t += clusters, ++i) {
+            const WideTile tile = wide_tile(p, t);
+            const int row0 = tile.n0 + 128 * rank + 32 * wq, o0 = tile.o0;
+            // groups of 64 channels of this warp: half, half + 2
+            const int groups = row0 < p.n_tok ? (min(tile.cols, p.d_out - o0) + 63) / 64 : 0;
+            const int last = groups > half + 2 ? half + 2 : half;
             const int b = i & 1;
             ptx::named_bar_sync(1, 256);   // every warp has read the last tile's scales
             scales[st] = o0 + st < p.d_out ? p.w_scale[o0 + st] : 0.f;
@@ -390,14 +415,13 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int q = 2 * half; q < 2 * half + 2; ++q) {
-                if (!ok || row0 >= p.n_tok || o0 + 64 * q >= p.d_out) break;   // the same for the whole warp
+            for (int q = half; q < groups && ok; q += 2) {   // the same for the whole warp
                 uint32_t r[2][32];
                 const uint32_t src = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 256 * b + 64 * q;
                 ptx::tmem_ld32(src, r[0]);
                 ptx::tmem_ld32(src + 32, r[1]);
                 ptx::tmem_wait_ld();
-                if (q & 1) {   // the accumulator has been read: the MMAs may have it back
+                if (q == last) {   // the accumulator has been read: the MMAs may have it back
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
@@ -424,8 +448,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                     ptx::bulk_commit_group();
                 }
             }
-            // a warp that did not read its last columns hands the accumulator back here
-            if (!ok || row0 >= p.n_tok || o0 + 64 * (2 * half + 1) >= p.d_out) {
+            if (groups <= half || !ok) {   // a warp without columns here
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
@@ -451,22 +474,30 @@ bool use_wide(int n_tok, int d_out) {
 cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
                          uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
     SplitArgs p;
-    // Token tiles of 256, or of 128 or 64 where that leaves half the SMs without
-    // a tile (897 tokens through 272 x 464: 26.3 us with 256).
     const int o_tiles = (d_out + 127) / 128;
-    int most_tok = 256;
-    while (most_tok > 64 && static_cast<long>(o_tiles) * ((n_tok + most_tok - 1) / most_tok) < kSms / 2) most_tok /= 2;
-    const int tok_tiles = (n_tok + most_tok - 1) / most_tok;
-    p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
     p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
-    // The largest cluster (a power of two: others leave SMs of a GPC unused)
-    // that keeps all CTAs resident and gives each two chunks.  32 tokens through
-    // 16,384 x 5,120 (40 tiles), product alone: 30.0, 18.9 and 29.4 us with 2, 4
-    // and 7 parts.
+    // Token tile and K parts by an estimate in cycles: the loads of the busiest
+    // SM at 50 bytes a cycle, and for each wave of CTAs the latency of its first
+    // loads and its epilogue.  Parts are a power of two (others leave SMs of a
+    // GPC unused) of two chunks at least.  32 tokens through 16,384 x 5,120 (40
+    // channel tiles), product alone: 30.0, 18.9 and 29.4 us with 2, 4 and 7
+    // parts; 897 tokens through 272 x 464: 26 us with tiles of 256, 9 with 64.
+    long best = -1;
+    int tok_tiles = 1, parts = 1;
+    for (int most_tok = 256; most_tok >= 64; most_tok /= 2) {
+        const int tt = (n_tok + most_tok - 1) / most_tok;
+        const int nt = ((n_tok + tt - 1) / tt + 15) / 16 * 16;
+        const long stage = kOpBytes + static_cast<long>(nt) * kChunk;
+        const int slots = (nt <= 64 ? 2 : 1) * kSms;   // CTAs resident at once
+        for (int k = 1; k <= kMaxCluster && (k == 1 || 2 * k <= p.chunks); k *= 2) {
+            const long ctas = static_cast<long>(o_tiles) * tt * k, waves = (ctas + slots - 1) / slots;
+            const long loads = (p.chunks + k - 1) / k * stage / 50;
+            const long cost = (ctas > kSms ? loads * ctas / kSms : loads) + waves * (3000 + 10 * nt + 20 * nt / k);
+            if (best < 0 || cost < best) best = cost, tok_tiles = tt, parts = k;
+        }
+    }
+    p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
     const bool two = p.nt <= 64;   // two CTAs per SM
-    int parts = kMaxCluster;
-    while (parts > 1 && (static_cast<long>(o_tiles) * tok_tiles * parts > (two ? 2 : 1) * kSms || 2 * parts > p.chunks))
-        parts /= 2;
     const uint32_t stage = kOpBytes + static_cast<uint32_t>(p.nt) * kChunk;
     const int most = (p.chunks + parts - 1) / parts;   // chunks of one CTA
     p.stages = static_cast<int>((two ? kSplitRingHalf : kSplitRing) / stage);
@@ -493,16 +524,22 @@ cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const
     WideArgs p;
     p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
     p.m_tiles = (n_tok + 255) / 256;
-    p.tiles = p.m_tiles * ((d_out + 255) / 256);
+    const int tiles = p.m_tiles * ((d_out + 255) / 256);
+    const int most = kSms / 2, rest = tiles % most;
+    p.cut = tiles < most || rest == 0 ? 1 : (4 * rest <= most ? 4 : (2 * rest <= most ? 2 : 1));
+    p.whole = p.cut > 1 ? tiles - rest : tiles;
+    p.pieces = p.cut > 1 ? rest * p.cut : 0;
     p.x_scale = x_scale, p.w_scale = w_scale, p.status = status;
     p.n_tok = n_tok, p.d_out = d_out;
-    if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) || !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, 128) ||
+    if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) ||
+        !make_map_i8(&p.tm_w_cut, w8, d_in, d_out, d_in, 128 / p.cut) ||
+        !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, 128) ||
         !make_map_2d(&p.tm_out, out, d_out, n_tok, static_cast<uint64_t>(d_out) * 2, 64, 32))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> smem_set{0};
     const cudaError_t e = allow_smem_once(linear_i8_wide_kernel, static_cast<int>(kWideSmem), smem_set);
     if (e != cudaSuccess) return e;
-    const int clusters = p.tiles < kSms / 2 ? p.tiles : kSms / 2;
+    const int clusters = tiles < most ? tiles : most;
     return launch_pdl(linear_i8_wide_kernel, dim3(2 * clusters), dim3(kWideThreads), kWideSmem, stream, p);
 }
 

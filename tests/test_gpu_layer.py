@@ -148,7 +148,8 @@ def test_linear_scales_beyond_float32_products(M):
 
 
 @pytest.mark.parametrize("n,d_in,d_out", [(129, 144, 15368), (300, 272, 7696), (1030, 144, 3336), (5000, 64, 1032),
-                                          (256, 2064, 15360), (2048, 16, 2056)])
+                                          (256, 2064, 15360), (2048, 16, 2056), (514, 272, 6328), (1000, 144, 6648),
+                                          (514, 1040, 6400), (16384, 64, 8), (1300, 2320, 8000)])
 def test_linear_many_tokens(M, n, d_in, d_out):
     """Enough output tiles for the many-token kernel, whole and ragged ones."""
     g = _gen(n + d_in * 3 + d_out)
