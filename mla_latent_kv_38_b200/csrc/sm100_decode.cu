@@ -284,6 +284,8 @@ __device__ __forceinline__ int unit_of_page(const int32_t* pf, int U, int g) { r
 // falls in.  With max_splits = s > 0 it then moves up to the next allowed
 // cut, where unit u's P tiles are cut into k = min(s, P) pieces at
 // tf[u] + floor(j P / k), j = 0 .. k, so no unit lies in more than s ranges.
+// (A shared decode of few pages was no faster cut by single pages: the merge of
+// the additional partials takes what the shorter tiles save.)
 constexpr int kSegCost = 6;
 
 __device__ __forceinline__ int unit_cost(int tiles) { return 4 * tiles + (tiles > 0 ? kSegCost : 0); }
@@ -1343,15 +1345,19 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um
 // and lse = -inf.
 //
 // The partial rows were written by the decode kernel just before and are read
-// from L2 (ld.global.cg).  The first two slots' rows are fetched together with
-// the log-sum-exps, so that a row split in two takes two dependent round trips
-// (metadata, then everything else); further slots follow two at a time.
+// from L2 (ld.global.cg).  The first slots' rows are fetched together with the
+// log-sum-exps, so that a row split in two takes two dependent round trips
+// (metadata, then everything else); further slots follow kSlots at a time.
 // Blocks of 8 warps, at most 64 registers a thread: 4 blocks per SM, one wave
 // for the 4,096 rows of 32 split units.  (Blocks of 4 warps doubled the merge
 // at prefill sizes, where most of the U x 128 rows belong to whole units and
 // the time goes into scheduling blocks that exit at once; one wave of blocks
 // that walk the rows was no faster.)
-template <bool kShared>
+//
+// kWarps warps per row, 512 / kWarps columns each, with 2 kWarps partials on
+// their way at a time: one for many rows, four for the few rows of a small
+// shared decode, which may have dozens of partials each.
+template <bool kShared, int kWarps>
 __global__ void __launch_bounds__(256, kShared ? 3 : 4)
 mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restrict__ part_o,
                        const float* __restrict__ part_lse, uint16_t* __restrict__ out_latent,
@@ -1377,17 +1383,20 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
             return Place{r >> 7, r & 127, (k.b * um.T_q + k.t) * um.n_h + k.hb * 128 + (r & 127)};
         }
     };
-    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int kVec = 4 / kWarps;     // 16-byte vectors of a lane
+    constexpr int kSlots = 2 * kWarps;   // partials requested together
+    const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = warp / kWarps, first_vec = (warp % kWarps) * kVec * 32 + lane;
     if (r >= rows) return;
     const Place at = place(r);
     const int4 own = unit_meta[um.n_prefix + at.uo];
     int4 pre = make_int4(0, 0, 0, 0);
     if (kShared && um.n_prefix > 0) pre = unit_meta[r >> 7];
-    uint2* dst = reinterpret_cast<uint2*>(out_latent + static_cast<size_t>(at.out) * kDc) + lane;
+    uint2* dst = reinterpret_cast<uint2*>(out_latent + static_cast<size_t>(at.out) * kDc) + first_vec;
     if (own.x == 0) {   // the sequence's length is out of range
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint2(0, 0);
-        if (lane == 0) out_lse[at.out] = -INFINITY;
+        for (int k = 0; k < kVec; ++k) dst[32 * k] = make_uint2(0, 0);
+        if (first_vec == 0) out_lse[at.out] = -INFINITY;
         return;
     }
     const int n_pre = pre.z;
@@ -1400,16 +1409,17 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
     auto row_of = [&](int i) {
         return kShared && i < n_pre ? pre_row + static_cast<size_t>(i) * 128 : own_row + (i - n_pre) * own_step;
     };
-    auto load_pair = [&](float4 (&v)[2][4], int i) {   // partials i, i + 1 (zeros past the last)
-        const float4* a = reinterpret_cast<const float4*>(part_o + row_of(i) * kDc) + lane;
-        const float4* c = reinterpret_cast<const float4*>(part_o + row_of(min(i + 1, parts - 1)) * kDc) + lane;
+    auto load_slots = [&](float4 (&v)[kSlots][kVec], int i) {   // partials i ..
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[0][k] = __ldcg(a + 32 * k);
+        for (int w = 0; w < kSlots; ++w) {
+            if (i + w >= parts) break;
+            const float4* a = reinterpret_cast<const float4*>(part_o + row_of(i + w) * kDc) + first_vec;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[1][k] = i + 1 < parts ? __ldcg(c + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < kVec; ++k) v[w][k] = __ldcg(a + 32 * k);
+        }
     };
-    float4 v[2][4];
-    load_pair(v, 0);
+    float4 v[kSlots][kVec];
+    load_slots(v, 0);
     constexpr int kPer = ((kShared ? 2 : 1) * kClusters + 31) / 32;   // log-sum-exp of partial lane + 32 k
     float ls[kPer];
     float mx = -INFINITY;
@@ -1430,33 +1440,30 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
         for (int k = 1; k < kPer; ++k) l = (i >> 5) == k ? ls[k] : l;
         return w_of(__shfl_sync(0xffffffffu, l, i & 31));
     };
-    float acc[16];
+    float4 acc[kVec];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    for (int i = 0; i < parts; i += 2) {
-        if (i > 0) load_pair(v, i);
-        const float w0 = weight(i), w1 = i + 1 < parts ? weight(i + 1) : 0.f;
-        if (kShared) {   // a partial of weight zero holds nothing that the row sees
+    for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; i += kSlots) {
+        if (i > 0) load_slots(v, i);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (w0 == 0.f) v[0][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (w1 == 0.f) v[1][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kSlots; ++w) {
+            if (i + w >= parts) break;             // the same for the whole warp
+            const float g = weight(i + w);
+            if (kShared && g == 0.f) continue;   // a weight of zero: nothing that the row sees
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                acc[k].x = fmaf(g, v[w][k].x, acc[k].x);
+                acc[k].y = fmaf(g, v[w][k].y, acc[k].y);
+                acc[k].z = fmaf(g, v[w][k].z, acc[k].z);
+                acc[k].w = fmaf(g, v[w][k].w, acc[k].w);
             }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            acc[4 * k + 0] = fmaf(w1, v[1][k].x, fmaf(w0, v[0][k].x, acc[4 * k + 0]));
-            acc[4 * k + 1] = fmaf(w1, v[1][k].y, fmaf(w0, v[0][k].y, acc[4 * k + 1]));
-            acc[4 * k + 2] = fmaf(w1, v[1][k].z, fmaf(w0, v[0][k].z, acc[4 * k + 2]));
-            acc[4 * k + 3] = fmaf(w1, v[1][k].w, fmaf(w0, v[0][k].w, acc[4 * k + 3]));
         }
     }
     const float inv = z > 0.f ? 1.f / z : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        dst[32 * k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                                 pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-    if (lane == 0) out_lse[at.out] = z > 0.f ? mx + logf(z) : -INFINITY;
+    for (int k = 0; k < kVec; ++k)
+        dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (first_vec == 0) out_lse[at.out] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1618,7 +1625,9 @@ cudaError_t launch_units(const DecodeParams& P, const UnitMap& um, int U, size_t
     e = launch_pdl(mla_decode_sm100_kernel<kShared>, dim3(2 * kClusters), dim3(kThreads), kSmemBytes, stream, k);
     if (e != cudaSuccess) return e;
     const int rows = kShared ? um.n_rows : U * 128;
-    return launch_pdl(mla_sm100_merge_kernel<kShared>, dim3((rows + 7) / 8), dim3(256), 0, stream,
+    const bool few = kShared && rows <= 148 * 8;   // four warps a row still make one wave
+    return launch_pdl(few ? mla_sm100_merge_kernel<kShared, kShared ? 4 : 1> : mla_sm100_merge_kernel<kShared, 1>,
+                      dim3(few ? (rows + 1) / 2 : (rows + 7) / 8), dim3(256), 0, stream,
                       static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),
                       static_cast<const float*>(k.part_lse), P.out_latent, P.out_lse, um, rows);
 }
