@@ -5,16 +5,18 @@
 // read by TMA in chunks of 128 columns (128-byte swizzle); columns past d_in,
 // rows past n_tok and d_out read as zero.
 //
-// Two kernels, chosen by use_wide():
-//  * split: few tokens.  Bound by the weights' bytes.  A CTA takes 128 channels
-//    (MMA M) against up to 256 tokens (MMA N); the K axis is cut over the CTAs
-//    of a cluster, so that every SM streams weights even where there are fewer
-//    channel tiles than SMs, and the partial sums meet in distributed shared
-//    memory: no workspace, no second launch.
-//  * wide: many tokens.  Bound by the tensor cores.  Persistent clusters of two
-//    CTAs issue cta_group::2 MMAs of 256 tokens x 256 channels (each SM supplies
-//    half of each operand); two accumulators in tensor memory let the epilogue
-//    of one tile run under the MMAs of the next.
+// Two kernels:
+//  * split: few tokens, or few tiles.  Bound by the weights' bytes at decode
+//    sizes.  A CTA takes 128 channels (MMA M) against up to 256 tokens (MMA N);
+//    the K axis is cut over the CTAs of a cluster, so that every SM streams
+//    weights even where there are fewer tiles than SMs, and the partial sums
+//    meet in distributed shared memory: no workspace, no second launch.
+//  * wide: many tokens.  Persistent clusters of two CTAs issue cta_group::2 MMAs
+//    of 256 tokens x 256 channels (each SM supplies half of each operand); two
+//    accumulators in tensor memory let the epilogue of one tile run under the
+//    MMAs of the next.  Bound by what L2 delivers to the SMs: 2,048 tokens
+//    through 1,536 x 24,576 take 60 us, 606 MB of operand tiles at 10 TB/s, the
+//    tensor pipe 62 % busy (ncu).
 
 #include <cuda.h>
 
@@ -465,37 +467,57 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
     griddep_launch_dependents();
 }
 
-// Many tokens: enough 256 x 256 tiles to fill most of the 74 clusters.
-bool use_wide(int n_tok, int d_out) {
-    const long tiles = static_cast<long>((n_tok + 255) / 256) * ((d_out + 255) / 256);
-    return n_tok > 128 && tiles >= 60;
-}
+// ---------------------------------------------------------------------------
+// choice of kernel and shape, by estimates in cycles
+// ---------------------------------------------------------------------------
 
-cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
-                         uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
-    SplitArgs p;
+// Token tile and K parts of the split kernel: the loads of the busiest SM at 50
+// bytes a cycle, and for each wave of CTAs the latency of its first loads and
+// its epilogue.  Parts are a power of two (others leave SMs of a GPC unused) of
+// two chunks at least.  Products alone, measured: 32 tokens through 16,384 x
+// 5,120 (40 channel tiles) 30.0, 18.9 and 29.4 us with 2, 4 and 7 parts; 897
+// tokens through 272 x 464 (with the quantisation) 26 us with token tiles of
+// 256, 9 with 64.
+struct SplitPlan {
+    long cost;
+    int tok_tiles, parts;
+};
+
+SplitPlan split_plan(int n_tok, int chunks, int d_out) {
+    SplitPlan best{-1, 1, 1};
     const int o_tiles = (d_out + 127) / 128;
-    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
-    // Token tile and K parts by an estimate in cycles: the loads of the busiest
-    // SM at 50 bytes a cycle, and for each wave of CTAs the latency of its first
-    // loads and its epilogue.  Parts are a power of two (others leave SMs of a
-    // GPC unused) of two chunks at least.  32 tokens through 16,384 x 5,120 (40
-    // channel tiles), product alone: 30.0, 18.9 and 29.4 us with 2, 4 and 7
-    // parts; 897 tokens through 272 x 464: 26 us with tiles of 256, 9 with 64.
-    long best = -1;
-    int tok_tiles = 1, parts = 1;
-    for (int most_tok = 256; most_tok >= 64; most_tok /= 2) {
-        const int tt = (n_tok + most_tok - 1) / most_tok;
+    for (int most = 256; most >= 64; most /= 2) {
+        const int tt = (n_tok + most - 1) / most;
         const int nt = ((n_tok + tt - 1) / tt + 15) / 16 * 16;
         const long stage = kOpBytes + static_cast<long>(nt) * kChunk;
         const int slots = (nt <= 64 ? 2 : 1) * kSms;   // CTAs resident at once
-        for (int k = 1; k <= kMaxCluster && (k == 1 || 2 * k <= p.chunks); k *= 2) {
+        for (int k = 1; k <= kMaxCluster && (k == 1 || 2 * k <= chunks); k *= 2) {
             const long ctas = static_cast<long>(o_tiles) * tt * k, waves = (ctas + slots - 1) / slots;
-            const long loads = (p.chunks + k - 1) / k * stage / 50;
-            const long cost = (ctas > kSms ? loads * ctas / kSms : loads) + waves * (3000 + 10 * nt + 20 * nt / k);
-            if (best < 0 || cost < best) best = cost, tok_tiles = tt, parts = k;
+            const long in_wave = ctas < slots ? ctas : slots;
+            const long loads = (chunks + k - 1) / k * stage / 50 * (in_wave > kSms ? in_wave : kSms) / kSms;
+            const long cost = waves * (loads + 3000 + 10 * nt + 20 * nt / k);
+            if (best.cost < 0 || cost < best.cost) best = SplitPlan{cost, tt, k};
         }
     }
+    return best;
+}
+
+// The wide kernel: rounds of all clusters, 620 cycles a chunk (its two operand
+// chunks per SM at about 50 bytes a cycle).  At 5,120 columns, measured: 32
+// tiles (512 tokens, 4,096 channels) 16.9 us split and 17.8 wide, 60 tiles 33
+// and 19; at 512 columns 32 tiles 7.3 and 7.1, 80 tiles 20 and 10.
+long wide_cost(int n_tok, int chunks, int d_out) {
+    const long tiles = static_cast<long>((n_tok + 255) / 256) * ((d_out + 255) / 256);
+    return 6000 + (tiles + kSms / 2 - 1) / (kSms / 2) * (chunks * 620L + 500);
+}
+
+cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
+                         uint16_t* out, int n_tok, int d_in, int d_out, const SplitPlan& plan, int32_t* status,
+                         cudaStream_t stream) {
+    SplitArgs p;
+    const int o_tiles = (d_out + 127) / 128;
+    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    const int tok_tiles = plan.tok_tiles, parts = plan.parts;
     p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
     const bool two = p.nt <= 64;   // two CTAs per SM
     const uint32_t stage = kOpBytes + static_cast<uint32_t>(p.nt) * kChunk;
@@ -548,8 +570,11 @@ cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const
 cudaError_t launch_linear_i8(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8,
                              const float* w_scale, uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status,
                              cudaStream_t stream) {
-    return (use_wide(n_tok, d_out) ? launch_wide : launch_split)(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out,
-                                                                 status, stream);
+    const int chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    const SplitPlan plan = split_plan(n_tok, chunks, d_out);
+    if (wide_cost(n_tok, chunks, d_out) < plan.cost)
+        return launch_wide(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, status, stream);
+    return launch_split(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, plan, status, stream);
 }
 
 }  // namespace mla
