@@ -1136,6 +1136,10 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 ptx::tc_fence_after();
                 const float lsum = exchange(l_part, true);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                // A warp of half 0, which does not see every phase of the barrier
+                // above, may have passed it a tile early: the exchange orders it
+                // behind those of half 1.
+                ptx::tc_fence_after();
                 const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
                 const float lse = lsum > 0.f ? (m_used + __log2f(lsum)) * kLn2 : -INFINITY;
                 const bool whole = t.whole && !(kShared && p.um.n_prefix > 0);
@@ -1265,8 +1269,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
 // ---------------------------------------------------------------------------
 template <bool kShared>
 __global__ void __launch_bounds__(1024)
-mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um, int max_splits, int U, int32_t* __restrict__ prefix, int32_t* __restrict__ tprefix,
-                          int32_t* __restrict__ wprefix, int32_t* __restrict__ kv_out, int4* __restrict__ unit_meta,
+mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um, int max_splits, int U,
+                          int32_t* __restrict__ prefix, int32_t* __restrict__ tprefix, int32_t* __restrict__ wprefix,
+                          int32_t* __restrict__ kv_out, int4* __restrict__ unit_meta,
                           int4* __restrict__ cluster_info, int32_t* status) {
     __shared__ int warp_tot[3][32];
     __shared__ int carry[3];

@@ -404,3 +404,129 @@ def test_norm_rope_append_skips_invalid_tokens(M):
             else:
                 assert torch.equal(q_c[b], k["q"][b, :, :32])
 
+
+
+# ---- a layer's step: the operators one after the other ------------------------
+
+class Layer:
+    """One attention layer's serving step of a batch behind shared pages, every projection around the per-head ones
+    in 8-bit integers: norm, down projections, norm of the query latent, W^UQ, append, absorb_q, decode, up_v, W^O, and
+    the residual add with the next block's norm."""
+
+    D, CQ, DC, DR, DH = 1024, 256, 512, 64, 128
+
+    def __init__(self, M, n_h, B, T_q, n_shared, own):
+        g = _gen(n_h + B)
+        self.M, self.cfg, self.B, self.T_q, self.n_h, self.n = M, M.MlaConfig(n_h, self.DC, self.DH, self.DR), B, T_q, n_h, B * T_q
+        n, D = self.n, self.D
+        pages = n_shared + max((k + 63) // 64 for k in own)
+        self.mb, self.n_shared = pages, n_shared
+        blocks = n_shared + B * (pages - n_shared)
+        perm = torch.randperm(blocks, generator=g, device="cuda").int()
+        self.shared = perm[:n_shared].contiguous()
+        self.table = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
+        self.table[:, n_shared:] = perm[n_shared:].view(B, -1)
+        self.table[:, :n_shared] = self.shared                    # the append reads the whole row
+        self.pool = _n(g, blocks, 64, self.DC + self.DR)
+        lens = torch.tensor([64 * n_shared + k for k in own], device="cuda")
+        self.lens = lens.int()
+        self.pos = (lens[:, None] - T_q + torch.arange(T_q, device="cuda")).int().reshape(-1)
+        self.rope = M.mla_rope_table(self.DR, 10000.0, 64 * pages).cuda()
+        self.x, self.res = _n(g, n, D), _n(g, n, D) * 2
+        self.w_in, self.w_cq, self.w_kv, self.w_next = (1 + 0.1 * _n(g, k) for k in (D, self.CQ, self.DC, D))
+
+        def weight(o, i):
+            w = (_n(g, o, i).float() / i ** 0.5).bfloat16()
+            w8, sw = torch.empty(o, i, dtype=torch.int8, device="cuda"), torch.empty(o, device="cuda")
+            M.mla_quantize_i8(w, i, o, i, w8, sw)
+            return w8, sw
+        self.w_down = weight(self.CQ + self.DC + self.DR, D)
+        self.w_uq = weight(n_h * (self.DH + self.DR), self.CQ)
+        self.w_o = weight(D, n_h * self.DH)
+        self.w_uk, self.w_uv = ((_n(g, n_h, self.DH, self.DC).float() / self.DC ** 0.5).bfloat16() for _ in range(2))
+        bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        i8 = lambda *s: torch.zeros(*s, dtype=torch.int8, device="cuda")  # noqa: E731
+        f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+        self.r = dict(res1=bf(n, D), h8=i8(n, D), sh=f(n), down=bf(n, self.CQ + self.DC + self.DR), cq8=i8(n, self.CQ), scq=f(n),
+                      q=bf(n, n_h, self.DH + self.DR), q_c=bf(n, n_h, self.DH), q_r=bf(n, n_h, self.DR),
+                      q_abs=bf(n, n_h, self.DC), latent=bf(n, n_h, self.DC), lse=f(n, n_h), o=bf(n, n_h * self.DH),
+                      o8=i8(n, n_h * self.DH), so=f(n), u=bf(n, D), res2=bf(n, D), y=bf(n, D))
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.ws = torch.zeros(M.mla_decode_shared_workspace_bytes(self.cfg, B, T_q), dtype=torch.uint8, device="cuda")
+
+    def step(self, between=lambda: None):
+        M, r, n, D, CQ, n_h = self.M, self.r, self.n, self.D, self.CQ, self.n_h
+        W = CQ + self.DC + self.DR
+        calls = [
+            lambda: M.mla_block_norm(self.x, D, None, None, 0, 1.0, self.res, r["res1"], self.w_in, EPS, n, D, None, r["h8"], r["sh"]),
+            lambda: M.mla_linear_i8(r["h8"], D, r["sh"], *self.w_down, r["down"], n, D, W, self.status),
+            lambda: M.mla_block_norm(r["down"], W, None, None, 0, 1.0, None, None, self.w_cq, EPS, n, CQ, None, r["cq8"], r["scq"]),
+            lambda: M.mla_linear_i8(r["cq8"], CQ, r["scq"], *self.w_uq, r["q"], n, CQ, n_h * (self.DH + self.DR), self.status),
+            lambda: M.mla_norm_rope_append(self.cfg, r["q"], r["down"][:, CQ:], W, self.w_kv, EPS, self.pos, self.rope,
+                                           self.rope.shape[0], self.table, self.mb, self.pool, self.pool.shape[0], self.B,
+                                           self.T_q, r["q_c"], r["q_r"], self.status),
+            lambda: M.mla_absorb_q(self.cfg, r["q_c"], self.w_uk, r["q_abs"], n),
+            lambda: M.mla_decode_shared(self.cfg, r["q_abs"], r["q_r"], self.pool, self.pool.shape[0], self.shared, self.n_shared,
+                                        self.table, self.mb, self.lens, self.B, self.T_q, 0, self.ws, self.ws.numel(),
+                                        r["latent"], r["lse"]),
+            lambda: M.mla_up_v(self.cfg, r["latent"], self.w_uv, r["o"], n),
+            lambda: M.mla_quantize_i8(r["o"], n_h * self.DH, n, n_h * self.DH, r["o8"], r["so"]),
+            lambda: M.mla_linear_i8(r["o8"], n_h * self.DH, r["so"], *self.w_o, r["u"], n, n_h * self.DH, D, self.status),
+            lambda: M.mla_block_norm(r["u"], D, None, None, 0, 0.5, r["res1"], r["res2"], self.w_next, EPS, n, D, r["y"]),
+        ]
+        for call in calls:
+            call()
+            between()
+
+    def results(self):
+        torch.cuda.synchronize()
+        assert self.M.mla_read_status(self.status) == 0 and self.M.mla_read_status(self.ws) == 0
+        return {k: v.clone() for k, v in self.r.items()} | {"pool": self.pool.clone()}
+
+
+@pytest.mark.parametrize("n_h,B,T_q,n_shared,own", [(16, 6, 2, 5, [2, 70, 130, 64, 3, 200]), (128, 3, 1, 9, [1, 64, 300]),
+                                                    (16, 40, 4, 3, [4, 67, 100, 150] * 10)])
+def test_a_layers_step(M, n_h, B, T_q, n_shared, own):
+    a = Layer(M, n_h, B, T_q, n_shared, own)
+    a.step(torch.cuda.synchronize)                # one call at a time
+    want = a.results()
+    # each projection and norm against its own inputs in 64 bits (the decode has its own tests)
+    r = want
+    rr, y, r_mag, y_mag = _norm64(a.x, None, None, 1.0, a.res, a.w_in)
+    assert ((r["res1"].double() - rr).abs() <= BF * rr.abs() + 64 * F32 * r_mag).all()
+    # codes of a float32 value a few roundings away from y may fall one step apart, next to a half
+    assert ((r["h8"].double() - 127 * y / y.abs().amax(1, keepdim=True)).abs() <= 0.5 + 127 * 64 * F32 * (y_mag / y.abs().amax(1, keepdim=True))).all()
+    _check_linear(r["down"], r["h8"], r["sh"], *a.w_down)
+    _check_linear(r["q"].view(a.n, -1), r["cq8"], r["scq"], *a.w_uq)
+    _check_linear(r["u"], r["o8"], r["so"], *a.w_o)
+    assert torch.equal(r["q_c"], r["q"][:, :, :a.DH])
+    # the decode's output against the keys that the append wrote
+    keys = torch.cat([a.pool[a.shared.long()].reshape(-1, 576), a.pool[a.table[0, n_shared:].long()].reshape(-1, 576)]).double()
+    see = keys[:64 * n_shared + own[0]]           # sequence 0, its last token
+    q = torch.cat([r["q_abs"][T_q - 1], r["q_r"][T_q - 1]], 1).double()
+    s = q @ see.T / 192 ** 0.5
+    p = torch.softmax(s, 1)
+    err = (577 * F32 * (q.abs() @ see.abs().T) / 192 ** 0.5 + 4 * F32 * s.abs()).amax(1)[:, None]   # of a weight, through its score
+    o, mag = p @ see[:, :512], p @ see[:, :512].abs()
+    assert ((r["latent"][T_q - 1].double() - o).abs() <= (BF + 2 * err + 1e-4) * mag + BF * o.abs()).all()
+    rr, y, r_mag, y_mag = _norm64(r["u"], None, None, 0.5, r["res1"], a.w_next)
+    assert ((r["res2"].double() - rr).abs() <= BF * rr.abs() + 64 * F32 * r_mag).all()
+    assert ((r["y"].double() - y).abs() <= BF * y.abs() + 64 * F32 * y_mag).all()
+
+    def same(got):
+        for k, v in want.items():
+            assert torch.equal(v.view(torch.uint8) if v.dtype != torch.int8 else v, got[k].view(torch.uint8) if v.dtype != torch.int8 else got[k]), k
+    # back to back, and captured: the same bits, whatever overlaps
+    for v in a.r.values():
+        v.zero_()
+    a.step()
+    same(a.results())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+        a.step()
+    for v in a.r.values():
+        v.zero_()
+    for _ in range(3):
+        graph.replay()
+    same(a.results())
