@@ -733,9 +733,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             const int grp = lane >> 2, j = lane & 3;
             const bool active = grp < kSLaneGroups && j < 3;
             const int my_pg = 2 * static_cast<int>(rank) + (j & 1);
-            TileWalker<kShared> w, wa;
+            TileWalker<kShared> w;
             walker(w);
-            walker(wa);
+            TileWalker<kShared> wa = w;
             int b0 = 0, b1 = 0, b2 = 0;
             bool h0 = false, h1 = false, h2 = false;
             // (the loads are unconditional, to a valid entry, so that nothing waits
@@ -786,9 +786,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             // different threads.  Lane pg < 4 holds the block of page pg of the
             // current tile (v0) and of the next one (v1).
             const uint64_t pol_v = ptx::l2_policy_evict_first();   // last use of these lines
-            TileWalker<kShared> w, wa;
+            TileWalker<kShared> w;
             walker(w);
-            walker(wa);
+            TileWalker<kShared> wa = w;
             int v0 = 0, v1 = 0;
             auto look = [&](int& v) {
                 if (!wa.done()) {
