@@ -424,9 +424,10 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                 ptx::tmem_ld32(src + 32, r[1]);
                 ptx::tmem_wait_ld();
                 if (q == last) {   // the accumulator has been read: the MMAs may have it back
+                    // (relaxed: a cluster-scope release held the warp for over 2,000 cycles)
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+                    if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(W_ACC_FREE + b));
                 }
                 // 32 rows x 64 bf16 in the store box's swizzled layout
                 if (lane == 0) ptx::bulk_wait_read_all();   // the last store has read its box
@@ -453,7 +454,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             if (groups <= half || !ok) {   // a warp without columns here
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(leader_bar(W_ACC_FREE + b));
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(leader_bar(W_ACC_FREE + b));
             }
         }
         if (lane == 0) ptx::bulk_wait_all();

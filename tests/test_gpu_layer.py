@@ -167,7 +167,9 @@ def test_linear_many_tokens_strided_and_extreme(M):
     w8 = torch.full((7696, d_in), -128, dtype=torch.int8, device="cuda")
     w8[1::3] = 127
     sx = torch.rand(n, generator=_gen(1), device="cuda") + 0.5
-    sw = torch.rand(7696, generator=_gen(2), device="cuda") + 0.5
+    sw = torch.rand(7697, generator=_gen(2), device="cuda")[1:] + 0.5     # 4-byte aligned only
+    sw = torch.cat([sw[:1], sw])[1:]
+    assert sw.data_ptr() % 16 == 4
     _check_linear(_linear(M, x8, sx, w8, sw, ld=d_in + 48), x8, sx, w8, sw)
 
 
