@@ -177,7 +177,9 @@ block_norm_kernel(const BlockNormArgs a) {
 // half.  Taken with a factor 2^-21 too small and one as much too large the two
 // differ there, and next to there: then the codes are divided for (127 x is
 // exact, and the correctly rounded quotient meets a half only where the exact
-// one does).  The kernel is bound by these instructions, not by its 3 bytes a
+// one does).  127 x leaves float32's range from 2^121 on, so the division takes
+// large rows 2^-32 times as large: what that rounds off lies 2^200 below the
+// maximum.  The kernel is bound by these instructions, not by its 3 bytes a
 // value: with a division each 40 us for 2,048 rows of 16,384, whose bytes take
 // 15.
 struct CodeFactor {
@@ -199,9 +201,10 @@ __device__ __forceinline__ uint2 quantize8(const uint4& w, const CodeFactor& c) 
         differ |= __float_as_uint(r[e]) ^ __float_as_uint(__fmaf_rn(f[e], c.hi, kRound));
     }
     if (differ) {
+        const float k = c.amax > 0x1p100f ? 0x1p-32f : 1.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            r[e] = __fadd_rn(c.amax > 0.f ? __fdiv_rn(127.f * f[e], c.amax) : 0.f, kRound);
+            r[e] = __fadd_rn(c.amax > 0.f ? __fdiv_rn(127.f * (k * f[e]), k * c.amax) : 0.f, kRound);
     }
     return pack_codes(r);
 }
