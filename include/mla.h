@@ -453,9 +453,12 @@ int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const in
  *   residual (n_tok, d) bf16;  residual_out (n_tok, d) bf16 receives r; it may
  *     be NULL, residual itself, or (with residual NULL) must be NULL
  *   out  (n_tok, d) bf16 receives y;  out8 (n_tok, d) int8 and out8_scale
- *     (n_tok) receive y quantised by the rule of mla_quantize_i8 from its
- *     float32 value.  Any of the three outputs may be NULL, not all; out and
- *     out8 need w_pre, and w_pre needs one of them.
+ *     (n_tok) receive y quantised by the rule of mla_quantize_i8 from float32
+ *     values: the codes from r w_pre, which the norm only scales, and the
+ *     scale from y's largest magnitude.  Any of the three outputs may be NULL,
+ *     not all; out and out8 need w_pre, and w_pre needs one of them.  Rows of
+ *     x and r are finite, with sums of squares in float32's range (below
+ *     3.4e38), and so is r w_pre.
  * d a multiple of 8, 8 <= d <= 16384 (out8: a multiple of 16); ld_u >= d, ld_gate
  * 0 or >= d, both multiples of 8; bf16 and int8 pointers 16-byte aligned; eps > 0;
  * alpha finite.  1 <= n_tok <= 2^24.  Outputs may not overlap inputs, other

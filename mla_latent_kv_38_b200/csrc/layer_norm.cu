@@ -145,22 +145,28 @@ block_norm_kernel(const BlockNormArgs a) {
         if (a.w_pre != nullptr) {
             const float2 tot = row_reduce<kWarpRow>(s, m, red, turn);
             rstd = rsqrtf(tot.x * inv_d + a.eps);
-            // the norm's factor is common to the row: the codes follow from r w_pre alone
-            const float inv = tot.y > 0.f ? __fdiv_rn(127.f, tot.y) : 0.f;
+            // the norm's factor is common to the row: the codes follow from r w_pre
+            // alone, taken 2^64 times as large where 127 / max would overflow
+            const bool tiny = tot.y < 0x1p-100f;
+            const float inv = tot.y > 0.f ? __fdiv_rn(127.f, tiny ? tot.y * 0x1p64f : tot.y) : 0.f;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int j = t + k * T;
                 if (j >= nv) continue;
                 float c[8];
-                if (a.out8 != nullptr) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) c[e] = __fadd_rn(x[k][e] * inv, kRound);
-                    reinterpret_cast<uint2*>(a.out8 + row * a.d)[j] = pack_codes(c);
-                }
                 if (a.out != nullptr) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) c[e] = x[k][e] * rstd;
                     reinterpret_cast<uint4*>(a.out + row * a.d)[j] = pack8(c);
+                }
+                if (a.out8 != nullptr) {
+                    if (tiny) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[k][e] *= 0x1p64f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) c[e] = __fadd_rn(x[k][e] * inv, kRound);
+                    reinterpret_cast<uint2*>(a.out8 + row * a.d)[j] = pack_codes(c);
                 }
             }
             if (a.out8 != nullptr && t == 0) a.out8_scale[row] = __fdiv_rn(tot.y * rstd, 127.f);
