@@ -203,6 +203,8 @@ size_t mla_decode_workspace_bytes(const mla_config_t* cfg, int B, int T_q, int m
  * Partial results (fp32 latent rows and log-sum-exp) of split rows go to the
  * workspace and are merged by a log-sum-exp reduction kernel.  The workspace
  * starts with the device status word (mla_read_status).
+ * A key whose score is NaN or +inf makes the latent and the lse of the rows
+ * that see it NaN.
  * Sizes: B * T_q <= 65535 query rows (and B * T_q * n_h / 128 <= 65535 units
  * on the tcgen05 kernels).  T_q > 1 with the generalised mask is also chunked
  * prefill ([notes] "MLA 코드 구현", "학습 시와 디코딩 시의 흐름"): a chunk of

@@ -314,7 +314,7 @@ merge_splits_kernel(const float* __restrict__ part_o, const float* __restrict__ 
         const float ls = part_lse[static_cast<size_t>(s) * rows + row];
         z += (ls == -INFINITY) ? 0.f : ex2((ls - m) * kLog2e);
     }
-    const float inv_z = z > 0.f ? 1.f / z : 0.f;
+    const float inv_z = z == 0.f ? 0.f : 1.f / z;
     for (int c = threadIdx.x * 4; c < d_c; c += blockDim.x * 4) {
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         for (int s = 0; s < splits; ++s) {
@@ -331,7 +331,7 @@ merge_splits_kernel(const float* __restrict__ part_o, const float* __restrict__ 
         pk.y = pack_bf16x2(a2, a3);
         *reinterpret_cast<uint2*>(out_latent + static_cast<size_t>(row) * d_c + c) = pk;
     }
-    if (threadIdx.x == 0) out_lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
+    if (threadIdx.x == 0) out_lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
 size_t simt_smem_bytes(int d_c, int d_r, bool e4m3) {

@@ -1140,8 +1140,10 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 // above, may have passed it a tile early: the exchange orders it
                 // behind those of half 1.
                 ptx::tc_fence_after();
-                const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-                const float lse = lsum > 0.f ? (m_used + __log2f(lsum)) * kLn2 : -INFINITY;
+                // zero: the row sees none of these keys.  A NaN (a score of NaN or +inf)
+                // stays one in the lse, so that the merge cannot weigh it away.
+                const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+                const float lse = lsum == 0.f ? -INFINITY : (m_used + __log2f(lsum)) * kLn2;
                 const bool whole = t.whole && !(kShared && p.um.n_prefix > 0);
                 const size_t grow = static_cast<size_t>(t.row0) + unit_row;
                 // the first row of the unit's partial slot
@@ -1453,8 +1455,7 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
 #pragma unroll
         for (int w = 0; w < kSlots; ++w) {
             if (i + w >= parts) break;             // the same for the whole warp
-            const float g = weight(i + w);
-            if (kShared && g == 0.f) continue;   // a weight of zero: nothing that the row sees
+            const float g = weight(i + w);   // zero: a finite row, or nothing that the row sees, which is zero too
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 acc[k].x = fmaf(g, v[w][k].x, acc[k].x);
@@ -1464,11 +1465,11 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
             }
         }
     }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
     for (int k = 0; k < kVec; ++k)
         dst[32 * k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-    if (first_vec == 0) out_lse[at.out] = z > 0.f ? mx + logf(z) : -INFINITY;
+    if (first_vec == 0) out_lse[at.out] = z == 0.f ? -INFINITY : mx + logf(z);
 }
 
 // ---------------------------------------------------------------------------
