@@ -222,8 +222,9 @@ decode_simt_kernel(DecodeParams P) {
         for (int h = 0; h < kHeadsPerWarp; ++h) {
             if (key >= kv_len) s[h] = -INFINITY;
             const float m_new = fmaxf(m_run[h], warp_max(s[h]));   // finite: key kt * 32 is visible
-            const float alpha = ex2(m_run[h] - m_new);
-            p[h] = ex2(s[h] - m_new);
+            const float base = kShared && m_new == -INFINITY ? 0.f : m_new;   // (all scores -inf: no weight)
+            const float alpha = ex2(m_run[h] - base);
+            p[h] = ex2(s[h] - base);
             l_run[h] = l_run[h] * alpha + warp_sum(p[h]);
             m_run[h] = m_new;
 #pragma unroll
@@ -239,7 +240,10 @@ decode_simt_kernel(DecodeParams P) {
                 pj[h] = __shfl_sync(0xffffffffu, p[h], j);
                 any = any || pj[h] != 0.f;
             }
-            if (!any) continue;   // warp-uniform
+            // warp-uniform; the shared decode takes every visible key, so that an
+            // infinity whose score of -inf gave it no weight shows (0 inf is NaN)
+            // whatever the weights of the warp's other rows
+            if (kShared ? kt * kSimtKeys + j >= kv_len : !any) continue;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ch = lane + 32 * u;
@@ -263,7 +267,13 @@ decode_simt_kernel(DecodeParams P) {
         bool empty = l_run[h] == 0.f;
         if (kShared && prefix) {   // rows of an invalid sequence see nothing
             const int rl = P.seq_lens[row / P.n_h / P.T_q];
-            empty = empty || rl < P.T_q + own0 || rl > P.max_blocks * P.block_size;
+            if (rl < P.T_q + own0 || rl > P.max_blocks * P.block_size) {
+                empty = true;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[h][u][k] = 0.f;
+            }
         }
         const float inv_l = empty ? 0.f : 1.f / l_run[h];
         const float lse = empty ? -INFINITY : (m_run[h] + __log2f(l_run[h])) * kLn2;
@@ -319,8 +329,7 @@ merge_splits_kernel(const float* __restrict__ part_o, const float* __restrict__ 
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         for (int s = 0; s < splits; ++s) {
             const float ls = part_lse[static_cast<size_t>(s) * rows + row];
-            if (ls == -INFINITY) continue;
-            const float w = ex2((ls - m) * kLog2e) * inv_z;
+            const float w = ls == -INFINITY ? 0.f : ex2((ls - m) * kLog2e) * inv_z;
             const float4 v = *reinterpret_cast<const float4*>(
                 part_o + (static_cast<size_t>(s) * rows + row) * d_c + c);
             a0 = fmaf(w, v.x, a0); a1 = fmaf(w, v.y, a1);

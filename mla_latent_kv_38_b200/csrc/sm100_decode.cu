@@ -171,6 +171,7 @@ struct Sm100Params {
     float* part_lse;          // (C + U) slots x 128
     int32_t* status;
     const int32_t* shared_table;   // (n_shared) blocks of the shared pages (shared decode only)
+    const uint16_t* pool;          // for single rows (shared decode only)
     UnitMap um;
     int U, num_blocks, max_splits;
     int in_kernel_schedule;   // 1: each CTA computes the schedule; 0: the schedule kernel did
@@ -184,6 +185,20 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
     if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
     if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
     return v;
+}
+
+// NaN in each of the 32 values whose bf16 counterpart in `row` is not finite.
+__device__ __forceinline__ void nan_where_infinite(uint32_t (&o)[32], const uint16_t* row) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint4 v = reinterpret_cast<const uint4*>(row)[k];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if ((w[e] & 0x7F80u) == 0x7F80u) o[8 * k + 2 * e] = 0x7FC00000u;
+            if ((w[e] & 0x7F800000u) == 0x7F800000u) o[8 * k + 2 * e + 1] = 0x7FC00000u;
+        }
+    }
 }
 
 template <bool kCluster = false>
@@ -966,6 +981,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
         // this thread's row of the unit and the row's token in a unit of several
         const int unit_row = 64 * static_cast<int>(rank) + m;
         const int row_tok = kShared ? unit_row / p.um.n_h : 0;
+        bool saw_inf = false;   // a key that later tokens share scored -inf for this row (see the epilogue)
         // The four partial values of row m (both key halves, both column groups)
         // meet through shared memory: the four warps of 32 rows (group wq & 1)
         // write, wait for each other and read; a warp writes again only when all
@@ -979,9 +995,14 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             if (lane == 0) ptx::mbar_arrive(bar(BAR_X_FULL + xg));
             ok = ok && wait_bar(bar(BAR_X_FULL + xg), x_turn & 1, abort_flag, p.status, tmo);
             ++x_turn;
-            const float a = xmax[m], b = xmax[64 + m], c = xmax[128 + m], d = xmax[192 + m];
+            float a = xmax[m], b = xmax[64 + m], c = xmax[128 + m], d = xmax[192 + m];
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(BAR_X_FREE + xg));
+            if (kShared && sum) {   // the sums carry saw_inf of the row's threads in their signs
+                const uint32_t signs = __float_as_uint(a) | __float_as_uint(b) | __float_as_uint(c) | __float_as_uint(d);
+                saw_inf = (signs >> 31) != 0;
+                a = fabsf(a), b = fabsf(b), c = fabsf(c), d = fabsf(d);
+            }
             return sum ? a + b + c + d : fmaxf(fmaxf(a, b), fmaxf(c, d));
         };
         while (ok && !w.done()) {
@@ -992,6 +1013,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             if (t.first) {
                 m_used = -INFINITY;
                 l_part = 0.f;
+                if constexpr (kShared) saw_inf = false;
             }
             const int sb = i & 1;
             ok = wait_bar(bar(BAR_S_FULL + sb), (i >> 1) & 1, abort_flag, p.status, tmo);
@@ -1012,6 +1034,13 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
                     if (j >= nvalid) r[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+            }
+            if (kShared && t.n_tok > 1 && kPage * (t.page0 + t.np) > t.kv - (t.n_tok - 1)) {
+                // rows of the keys from t.kv - (n_tok - 1) on are cleaned below
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    saw_inf |= j < nvalid && key0 + j >= t.kv - (t.n_tok - 1) &&
+                               __uint_as_float(r[j >> 5][j & 31]) == -INFINITY;
             }
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // independent chains
 #pragma unroll
@@ -1110,7 +1139,9 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                     // Rows that only the unit's later tokens see: a weight of zero
                     // hides them from the earlier ones, unless they hold infinities
                     // or NaN, which are dropped here.  The tokens that do see such a
-                    // row have a score, and so an output, that is not finite.
+                    // row have a score that is not finite: NaN or +inf makes the
+                    // weight, and so the output, NaN; -inf a weight of zero, and the
+                    // epilogue puts NaN into the columns that lost an infinity.
                     const int from = max(0, left - (t.n_tok - 1)), part = valid - from;
                     for (int x = st; x < 4 * part * 8; x += 256) {
                         const int chunk = x / (part * 8);
@@ -1134,7 +1165,7 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                 ok = wait_bar(bar(BAR_P_FREE + 1), i & 1, abort_flag, p.status, tmo);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
-                const float lsum = exchange(l_part, true);
+                const float lsum = exchange(kShared && saw_inf ? -l_part : l_part, true);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 // A warp of half 0, which does not see every phase of the barrier
                 // above, may have passed it a tile early: the exchange orders it
@@ -1177,6 +1208,15 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
                     uint32_t o[32];
                     ptx::tmem_ld32(t_lane + kTmemO + 128 * h + 32 * q, o);
                     ptx::tmem_wait_ld();
+                    if constexpr (kShared) {
+                        // 0 inf = NaN for the cleaned infinities that this row sees
+                        // (rare: read again from the cache)
+                        if (saw_inf)
+                            for (int key = max(0, t.kv - (t.n_tok - 1)); key < t.kv - max(0, t.n_tok - 1 - row_tok); ++key)
+                                nan_where_infinite(o, p.pool + (static_cast<size_t>(blk_row(load_blk(t, key / kPage - t.page0))) +
+                                                                key % kPage) * kRow + col0 + 32 * q);
+                        __syncwarp();
+                    }
                     if (kShared && whole && warp_rows < 32) {
                         // the store's box would reach into another unit's rows
                         uint4* dst = reinterpret_cast<uint4*>(p.out_latent + grow * kDc + col0 + 32 * q);
@@ -1455,7 +1495,7 @@ mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restri
 #pragma unroll
         for (int w = 0; w < kSlots; ++w) {
             if (i + w >= parts) break;             // the same for the whole warp
-            const float g = weight(i + w);   // zero: a finite row, or nothing that the row sees, which is zero too
+            const float g = weight(i + w);   // (nothing is skipped at zero: 0 inf of a key at -inf stays NaN)
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
                 acc[k].x = fmaf(g, v[w][k].x, acc[k].x);
@@ -1596,6 +1636,7 @@ cudaError_t launch_units(const DecodeParams& P, const UnitMap& um, int U, size_t
         return cudaErrorInvalidValue;
     k.block_table = P.block_table;
     k.shared_table = P.shared_table;
+    k.pool = P.pool;
     k.seq_lens = P.seq_lens;
     k.prefix = reinterpret_cast<int32_t*>(base + w.prefix);
     k.unit_kv = reinterpret_cast<int32_t*>(base + w.kv);

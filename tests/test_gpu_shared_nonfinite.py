@@ -1,8 +1,11 @@
 """Infinities and NaN among the keys that a row of mla_decode_shared sees.
 
 A score that is NaN or +inf leaves neither a weight nor a log-sum-exp: the
-row's latent and lse are NaN, whichever key range they were computed in.
-mla_decode on the same cache gives the same.
+row's latent and lse are NaN, whichever key range they were computed in.  A
+score of -inf is a weight of zero; times the infinity in the key's latent that
+made it, it is NaN in that column (0 inf), and the other columns and the lse
+are those of the keys without it.  mla_decode on the same cache gives the same.
+Bounds of finite values as in test_gpu_shared.py.
 """
 
 import math
@@ -10,7 +13,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_shared import M, V2, Case  # noqa: F401
+from tests.test_gpu_shared import BF, M, SCORE, V2, Case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +90,49 @@ def test_mla_decode_agrees_on_nan_rows(M):  # noqa: F811
         assert torch.equal(torch.isnan(lat1[:n]).view_as(lat), torch.isnan(lat))
         assert torch.equal(torch.isnan(lse1[:n]).view_as(lse), torch.isnan(lse))
         assert torch.isnan(lat[2]).all() and torch.isnan(lse[2]).all() and torch.isfinite(lat[:2].float()).all()
+
+
+MINUS = [  # n_h, T_q, n_shared, own keys, the key's place before the sequence's end
+    (16, 4, 3, [4, 66, 131, 259], 2), (1, 70, 3, [70, 130, 200], 35), (128, 3, 3, [3, 66, 257], 1), (40, 3, 3, [64], 2),
+    (16, 4, 20, [70, 66, 131, 259], 66), (24, 9, 6, [9, 70, 64], 9), (16, 2, 0, [65, 200], 1), (16, 1, 9, [65, 200] * 6, 30)]
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("impl", [0, 1])
+@pytest.mark.parametrize("n_h,T_q,n_shared,own,back", MINUS)
+def test_a_score_of_minus_infinity(M, impl, n_h, T_q, n_shared, own, back, splits):  # noqa: F811
+    """An infinity in one latent column of one key, against a negative query: NaN in that column of the rows that see
+    the key, whatever else shares their unit of work; the rest as if the key were not there."""
+    make = lambda: Case(M, n_h, *V2, T_q, n_shared, own, impl, splits)  # noqa: E731
+    clean = make()
+    clean.q_abs[:, :, COL] = -0.5
+    lat0, lse0 = (x.clone() for x in _run(clean))
+    c = make()
+    c.q_abs[:, :, COL] = -0.5
+    at = [64 * n_shared + k - back for k in own]
+    for b in range(len(own)):
+        _put(c, b, at[b], math.inf)
+    lat, lse = _run(c)
+    prefix = c.pool[c.shared.long()].reshape(-1, 576)
+    scale = 1.0 / math.sqrt(192)
+    for b, k in enumerate(own):
+        ids = c.table[b, n_shared:(64 * n_shared + k + 63) // 64].long()
+        keys = torch.cat([prefix, c.pool[ids].reshape(-1, 576)[:k]]).double()
+        for t in range(T_q):
+            last = 64 * n_shared + k - T_q + t
+            # keys at infinity that this row sees: its sequence's own, and those of the others put among shared keys
+            hit = ~torch.isfinite(keys[:last + 1, COL])
+            if not hit.any():
+                assert torch.equal(lat[b, t], lat0[b, t]) and torch.equal(lse[b, t], lse0[b, t]), (b, t)
+                continue
+            assert torch.isnan(lat[b, t, :, COL]).all(), (b, t)
+            see = keys[:last + 1][~hit]
+            n = b * T_q + t
+            s = torch.cat([c.q_abs[n], c.q_r[n]], 1).double() @ see.T * scale
+            want = torch.logsumexp(s, 1)
+            p = torch.exp(s - want[:, None])
+            o, mag = p @ see[:, :512], p @ see[:, :512].abs()
+            rest = torch.arange(512, device="cuda") != COL
+            err = (lat[b, t].double() - o).abs()
+            assert (err <= (BF + SCORE) * mag + BF * o.abs())[:, rest].all(), (b, t)
+            assert ((lse[b, t].double() - want).abs() <= SCORE).all(), (b, t)
