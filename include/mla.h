@@ -441,6 +441,12 @@ int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const in
                   const float* w_scale, mla_bf16* out, int n_tok, int d_in, int d_out,
                   int32_t* dev_status, void* stream);
 
+/* Diagnostic, on the host alone: what a block of the kernel that mla_linear_i8
+ * picks for these sizes holds while it runs -- the CTAs of its cluster, its
+ * tensor-memory columns (of 512 an SM) and its dynamic shared memory (of 228 KB
+ * an SM, with 1 KB more a block). */
+int mla_linear_i8_shape(int n_tok, int d_in, int d_out, int* cluster, int* tmem_cols, size_t* smem_bytes);
+
 /* The end of one block and the norm in front of the next, in one pass over
  * each token's row (float32 throughout, each output rounded once):
  *   x = u                                            (the block's output)

@@ -32,6 +32,7 @@ EXPORTED = (
     "mla_fold_weights", "mla_absorb_q_folded", "mla_up_o_folded_workspace_bytes", "mla_up_o_folded",
     "mla_e4m3_row_bytes", "mla_rope_append_e4m3", "mla_decode_e4m3_workspace_bytes", "mla_decode_e4m3",
     "mla_decode_shared_workspace_bytes", "mla_decode_shared", "mla_quantize_i8", "mla_linear_i8",
+    "mla_linear_i8_shape",
     "mla_block_norm", "mla_norm_rope_append", "mla_norm_rope_append_e4m3",
     "mla_clear_status", "mla_read_status",
 )
@@ -106,6 +107,7 @@ _lib.mla_decode_shared.argtypes = [_cfgp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _
                                    _vp]
 _lib.mla_quantize_i8.argtypes = [_vp, _i64, _i, _i, _vp, _vp, _vp]
 _lib.mla_linear_i8.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
+_lib.mla_linear_i8_shape.argtypes = [_i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i), ctypes.POINTER(_sz)]
 _lib.mla_block_norm.argtypes = [_vp, _i64, _vp, _vp, _i64, _f, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _vp, _vp]
 _lib.mla_norm_rope_append.argtypes = [_cfgp, _vp, _vp, _i64, _vp, _f, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp,
                                       _vp, _vp]
@@ -324,6 +326,14 @@ def mla_linear_i8(x8, ld_x: int, x_scale, w8, w_scale, out, n_tok: int, d_in: in
     """out = (x8 w8^T) x_scale w_scale in bf16: an int8 projection with scales per token and output channel."""
     _check("mla_linear_i8", _lib.mla_linear_i8(_ptr(x8), ld_x, _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(out),
                                                n_tok, d_in, d_out, _ptr(dev_status), _stream(stream)))
+
+
+def mla_linear_i8_shape(n_tok: int, d_in: int, d_out: int):
+    """(CTAs of a cluster, tensor-memory columns, dynamic shared-memory bytes) of the kernel mla_linear_i8 picks."""
+    cluster, cols, smem = _i(0), _i(0), _sz(0)
+    _check("mla_linear_i8_shape", _lib.mla_linear_i8_shape(n_tok, d_in, d_out, ctypes.byref(cluster), ctypes.byref(cols),
+                                                           ctypes.byref(smem)))
+    return cluster.value, cols.value, smem.value
 
 
 def mla_block_norm(u, ld_u: int, w_post, gate, ld_gate: int, alpha: float, residual, residual_out, w_pre, eps: float,

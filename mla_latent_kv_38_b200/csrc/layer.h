@@ -32,6 +32,14 @@ cudaError_t launch_linear_i8(const int8_t* x8, long ld_x, const float* x_scale, 
                              const float* w_scale, uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status,
                              cudaStream_t stream);
 
+// What a block of the kernel that launch_linear_i8 picks holds: CTAs of a
+// cluster, tensor-memory columns and dynamic shared memory.
+struct LinearShape {
+    int cluster, tmem_cols;
+    size_t smem;
+};
+LinearShape linear_i8_shape(int n_tok, int d_in, int d_out);
+
 // pool: bf16 rows of d_c + d_r values, or (e4m3) rows in the layout of
 // mla_e4m3_row_bytes; q, q_c and q_r may be null together
 cudaError_t launch_norm_rope_append(const uint16_t* q, const uint16_t* kv, long ld_kv, const uint16_t* w_kv, float eps,

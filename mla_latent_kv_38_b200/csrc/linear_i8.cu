@@ -72,6 +72,12 @@ __device__ __forceinline__ float scaled(int sum, float sx, float sw) { return st
 // split
 // ---------------------------------------------------------------------------
 
+// Dynamic shared memory at which blocks with `cols` columns of tensor memory
+// fill the SM's shared memory (1 KB of it reserved per block) no later than its
+// 512 columns, alone or mixed with others that keep to this.
+constexpr size_t kSmSmem = 233472;
+constexpr size_t tmem_share(uint32_t cols) { return kSmSmem / 512 * cols - 1024; }
+
 constexpr int kSplitThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kSplitRing = 200 * 1024;       // one CTA per SM
@@ -254,8 +260,8 @@ constexpr uint32_t kOffScales = kOffStage + 8 * 4096;      // the tile's 256 cha
 constexpr uint32_t kOffWideBars = kOffScales + 1024;
 enum { W_FULL = 0, W_EMPTY = W_FULL + kWideStages, W_ACC_FULL = W_EMPTY + kWideStages, W_ACC_FREE = W_ACC_FULL + 2,
        W_DRAIN = W_ACC_FREE + 2, W_BARS = W_DRAIN + 1 };
-constexpr uint32_t kWideSmem = kOffWideBars + 8 * W_BARS + 16 + 1024;
-static_assert(kWideSmem <= 232448, "shared memory budget");
+constexpr uint32_t kWideSmem = 232448;   // all of it, with all of the tensor memory
+static_assert(kOffWideBars + 8 * W_BARS + 16 + 1024 <= kWideSmem && kWideSmem >= tmem_share(512), "shared memory budget");
 
 struct WideArgs {
     CUtensorMap tm_x;     // x8 [n_tok][d_in], boxes 128 x 128
@@ -512,40 +518,63 @@ long wide_cost(int n_tok, int chunks, int d_out) {
     return 6000 + (tiles + kSms / 2 - 1) / (kSms / 2) * (chunks * 620L + 500);
 }
 
+int chunks_of(int d_in) { return (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk); }
+
+// Launch shape of the split kernel.  Its dynamic shared memory is at least its
+// tensor memory's share of an SM: tcgen05.alloc waits without a bound for free
+// columns, and the CTAs of a cluster for each other, so clusters that waited
+// for one another's columns on different SMs would wait forever.  Blocks that
+// fit an SM together never ask for more than its columns.  (The decode keeps to
+// the same rule; the projections' CTAs need no others to finish.)
+struct SplitShape {
+    int nt, stages;              // tokens of a tile, ring stages
+    uint32_t ring_bytes, tmem_cols;
+    size_t smem;                 // dynamic shared memory
+};
+
+SplitShape split_shape(int n_tok, int chunks, const SplitPlan& plan) {
+    SplitShape s;
+    s.nt = ((n_tok + plan.tok_tiles - 1) / plan.tok_tiles + 15) / 16 * 16;
+    const bool two = s.nt <= 64;   // two CTAs per SM
+    const uint32_t stage = kOpBytes + static_cast<uint32_t>(s.nt) * kChunk;
+    const int most = (chunks + plan.parts - 1) / plan.parts;   // chunks of one CTA
+    s.stages = static_cast<int>((two ? kSplitRingHalf : kSplitRing) / stage);
+    if (s.stages > most) s.stages = most;
+    s.ring_bytes = s.stages * stage;
+    if (s.ring_bytes < static_cast<uint32_t>(s.nt) * 512) s.ring_bytes = static_cast<uint32_t>(s.nt) * 512;
+    s.tmem_cols = 32;
+    while (s.tmem_cols < static_cast<uint32_t>(s.nt)) s.tmem_cols *= 2;
+    s.smem = s.ring_bytes + 8 * (2 * s.stages + 1) + 16 + 1024;
+    const size_t least = tmem_share(s.tmem_cols);
+    if (s.smem < least) s.smem = least;
+    return s;
+}
+
 cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
                          uint16_t* out, int n_tok, int d_in, int d_out, const SplitPlan& plan, int32_t* status,
                          cudaStream_t stream) {
     SplitArgs p;
     const int o_tiles = (d_out + 127) / 128;
-    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    p.chunks = chunks_of(d_in);
     const int tok_tiles = plan.tok_tiles, parts = plan.parts;
-    p.nt = ((n_tok + tok_tiles - 1) / tok_tiles + 15) / 16 * 16;
-    const bool two = p.nt <= 64;   // two CTAs per SM
-    const uint32_t stage = kOpBytes + static_cast<uint32_t>(p.nt) * kChunk;
-    const int most = (p.chunks + parts - 1) / parts;   // chunks of one CTA
-    p.stages = static_cast<int>((two ? kSplitRingHalf : kSplitRing) / stage);
-    if (p.stages > most) p.stages = most;
-    p.ring_bytes = p.stages * stage;
-    if (p.ring_bytes < static_cast<uint32_t>(p.nt) * 512) p.ring_bytes = static_cast<uint32_t>(p.nt) * 512;
-    p.tmem_cols = 32;
-    while (p.tmem_cols < static_cast<uint32_t>(p.nt)) p.tmem_cols *= 2;
+    const SplitShape shape = split_shape(n_tok, p.chunks, plan);
+    p.nt = shape.nt, p.stages = shape.stages, p.ring_bytes = shape.ring_bytes, p.tmem_cols = shape.tmem_cols;
     p.idesc = ptx::idesc_i8_s32(128, p.nt);
     p.x_scale = x_scale, p.w_scale = w_scale, p.out = out, p.status = status;
     p.n_tok = n_tok, p.d_out = d_out;
     if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) || !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, p.nt))
         return cudaErrorInvalidValue;
-    const size_t smem = p.ring_bytes + 8 * (2 * p.stages + 1) + 16 + 1024;
     static std::atomic<uint64_t> smem_set{0};
     const cudaError_t e = allow_smem_once(linear_i8_split_kernel, static_cast<int>(kSplitRing + 2048), smem_set);
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(linear_i8_split_kernel, dim3(o_tiles * parts, tok_tiles), dim3(kSplitThreads), parts, smem,
+    return launch_pdl_cluster(linear_i8_split_kernel, dim3(o_tiles * parts, tok_tiles), dim3(kSplitThreads), parts, shape.smem,
                               stream, p);
 }
 
 cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8, const float* w_scale,
                         uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status, cudaStream_t stream) {
     WideArgs p;
-    p.chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
+    p.chunks = chunks_of(d_in);
     p.m_tiles = (n_tok + 255) / 256;
     const int tiles = p.m_tiles * ((d_out + 255) / 256);
     const int most = kSms / 2, rest = tiles % most;
@@ -568,14 +597,30 @@ cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const
 
 }  // namespace
 
+namespace {
+
+// The kernel that serves a product: wide, or split with this plan.
+bool choose_wide(int n_tok, int chunks, int d_out, SplitPlan* plan) {
+    *plan = split_plan(n_tok, chunks, d_out);
+    return wide_cost(n_tok, chunks, d_out) < plan->cost;
+}
+
+}  // namespace
+
 cudaError_t launch_linear_i8(const int8_t* x8, long ld_x, const float* x_scale, const int8_t* w8,
                              const float* w_scale, uint16_t* out, int n_tok, int d_in, int d_out, int32_t* status,
                              cudaStream_t stream) {
-    const int chunks = (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk);
-    const SplitPlan plan = split_plan(n_tok, chunks, d_out);
-    if (wide_cost(n_tok, chunks, d_out) < plan.cost)
+    SplitPlan plan;
+    if (choose_wide(n_tok, chunks_of(d_in), d_out, &plan))
         return launch_wide(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, status, stream);
     return launch_split(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, plan, status, stream);
+}
+
+LinearShape linear_i8_shape(int n_tok, int d_in, int d_out) {
+    SplitPlan plan;
+    if (choose_wide(n_tok, chunks_of(d_in), d_out, &plan)) return LinearShape{2, 512, kWideSmem};
+    const SplitShape s = split_shape(n_tok, chunks_of(d_in), plan);
+    return LinearShape{plan.parts, static_cast<int>(s.tmem_cols), s.smem};
 }
 
 }  // namespace mla

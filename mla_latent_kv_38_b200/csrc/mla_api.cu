@@ -101,6 +101,11 @@ WsLayout ws_layout_shared(const mla_config_t* c, int B, int T_q, int max_splits)
 // Shapes of the e4m3 cache format: whole 64-column groups of the latent.
 bool e4m3_shape(const mla_config_t* c) { return c->d_c % MLA_E4M3_GROUP == 0; }
 
+bool linear_sizes_ok(int n_tok, int d_in, int d_out) {
+    if (n_tok < 1 || n_tok > 65536 || d_in < 16 || d_in > 65536 || d_in % 16) return false;
+    return d_out >= 8 && d_out <= 131072 && d_out % 8 == 0;
+}
+
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_LAUNCH; }
 
 // Query rows of a decode call: B sequences x T_q tokens, T_q from 1 (decode)
@@ -579,12 +584,19 @@ int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const in
     if (!aligned16(x8) || !aligned16(w8) || !aligned16(out) || !aligned4(x_scale) || !aligned4(w_scale) ||
         (dev_status && !aligned4(dev_status)))
         return MLA_ERR_ALIGN;
-    if (n_tok < 1 || n_tok > 65536 || d_in < 16 || d_in > 65536 || d_in % 16) return MLA_ERR_SIZE;
-    if (d_out < 8 || d_out > 131072 || d_out % 8) return MLA_ERR_SIZE;
+    if (!linear_sizes_ok(n_tok, d_in, d_out)) return MLA_ERR_SIZE;
     if (ld_x < d_in || ld_x % 16 || ld_x > kMaxRowStride) return MLA_ERR_SIZE;
     if (mla_check_device() != MLA_OK) return MLA_ERR_UNSUPPORTED;
     return cuda_rc(mla::launch_linear_i8(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, dev_status,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+int mla_linear_i8_shape(int n_tok, int d_in, int d_out, int* cluster, int* tmem_cols, size_t* smem_bytes) {
+    if (!cluster || !tmem_cols || !smem_bytes) return MLA_ERR_NULL;
+    if (!linear_sizes_ok(n_tok, d_in, d_out)) return MLA_ERR_SIZE;
+    const mla::LinearShape s = mla::linear_i8_shape(n_tok, d_in, d_out);
+    *cluster = s.cluster, *tmem_cols = s.tmem_cols, *smem_bytes = s.smem;
+    return MLA_OK;
 }
 
 int mla_block_norm(const mla_bf16* u, int64_t ld_u, const mla_bf16* w_post, const mla_bf16* gate,
