@@ -103,8 +103,13 @@ rope_append_kernel(uint16_t* __restrict__ q_r, const uint16_t* __restrict__ k_r,
         const int p = positions[n];
         if (p < 0 || p >= max_pos || p / block_size >= max_blocks) return;   // flagged by the append
         uint16_t* q = q_r + ni * d_r;
-        const float4 c = *reinterpret_cast<const float4*>(table + static_cast<size_t>(p) * d_r + m);
-        const float4 sn = *reinterpret_cast<const float4*>(table + static_cast<size_t>(p) * d_r + h + m);
+        // (the table needs no more than a float's alignment)
+        const bool vec = (reinterpret_cast<uintptr_t>(table) & 15u) == 0;
+        auto four = [vec](const float* f) {
+            return vec ? *reinterpret_cast<const float4*>(f) : make_float4(f[0], f[1], f[2], f[3]);
+        };
+        const float4 c = four(table + static_cast<size_t>(p) * d_r + m);
+        const float4 sn = four(table + static_cast<size_t>(p) * d_r + h + m);
         const uint2 x1 = *reinterpret_cast<const uint2*>(q + m);
         const uint2 x2 = *reinterpret_cast<const uint2*>(q + h + m);
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
