@@ -434,7 +434,8 @@ int mla_quantize_i8(const mla_bf16* x, int64_t ld_x, int n_rows, int d, int8_t* 
  * W^DQ and W^DKV (one above the other), W^UQ, W^O, or the folded F and G.
  *   x8 (n_tok, d_in) int8, rows ld_x bytes apart (ld_x >= d_in, a multiple of
  *   16);  w8 (d_out, d_in) int8;  x_scale (n_tok), w_scale (d_out) float32
- *   out (n_tok, d_out) bf16;  dev_status as for mla_absorb_q
+ *   out (n_tok, d_out) bf16;  dev_status as for mla_absorb_q (out is undefined
+ *   where a wait ran out, and nothing else tells)
  * 1 <= n_tok <= 65536, 16 <= d_in <= 65536 and a multiple of 16, 8 <= d_out <=
  * 131072 and a multiple of 8.  x8, w8 and out are 16-byte aligned. */
 int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const int8_t* w8,
@@ -446,6 +447,12 @@ int mla_linear_i8(const int8_t* x8, int64_t ld_x, const float* x_scale, const in
  * tensor-memory columns (of 512 an SM) and its dynamic shared memory (of 228 KB
  * an SM, with 1 KB more a block). */
 int mla_linear_i8_shape(int n_tok, int d_in, int d_out, int* cluster, int* tmem_cols, size_t* smem_bytes);
+
+/* Test hook for the product's bounded waits, as mla_test_arm_decode_timeout: the
+ * NEXT mla_linear_i8 call never issues one of its loads and bounds every wait
+ * by wait_limit_ns (1 ns .. 2 s).  The call returns MLA_OK; the kernel unwinds
+ * and sets MLA_STATUS_TIMEOUT, and out is undefined.  Not for production use. */
+int mla_test_arm_linear_timeout(uint64_t wait_limit_ns);
 
 /* The end of one block and the norm in front of the next, in one pass over
  * each token's row (float32 throughout, each output rounded once):

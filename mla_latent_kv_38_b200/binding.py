@@ -32,7 +32,7 @@ EXPORTED = (
     "mla_fold_weights", "mla_absorb_q_folded", "mla_up_o_folded_workspace_bytes", "mla_up_o_folded",
     "mla_e4m3_row_bytes", "mla_rope_append_e4m3", "mla_decode_e4m3_workspace_bytes", "mla_decode_e4m3",
     "mla_decode_shared_workspace_bytes", "mla_decode_shared", "mla_quantize_i8", "mla_linear_i8",
-    "mla_linear_i8_shape",
+    "mla_linear_i8_shape", "mla_test_arm_linear_timeout",
     "mla_block_norm", "mla_norm_rope_append", "mla_norm_rope_append_e4m3",
     "mla_clear_status", "mla_read_status",
 )
@@ -108,6 +108,7 @@ _lib.mla_decode_shared.argtypes = [_cfgp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _
 _lib.mla_quantize_i8.argtypes = [_vp, _i64, _i, _i, _vp, _vp, _vp]
 _lib.mla_linear_i8.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
 _lib.mla_linear_i8_shape.argtypes = [_i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i), ctypes.POINTER(_sz)]
+_lib.mla_test_arm_linear_timeout.argtypes = _lib.mla_test_arm_decode_timeout.argtypes
 _lib.mla_block_norm.argtypes = [_vp, _i64, _vp, _vp, _i64, _f, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _vp, _vp]
 _lib.mla_norm_rope_append.argtypes = [_cfgp, _vp, _vp, _i64, _vp, _f, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp,
                                       _vp, _vp]
@@ -334,6 +335,12 @@ def mla_linear_i8_shape(n_tok: int, d_in: int, d_out: int):
     _check("mla_linear_i8_shape", _lib.mla_linear_i8_shape(n_tok, d_in, d_out, ctypes.byref(cluster), ctypes.byref(cols),
                                                            ctypes.byref(smem)))
     return cluster.value, cols.value, smem.value
+
+
+def mla_test_arm_linear_timeout(wait_limit_ns: int):
+    """Test hook: the next mla_linear_i8 call withholds one load and bounds its
+    waits by wait_limit_ns (it then reports MLA_STATUS_TIMEOUT)."""
+    _check("mla_test_arm_linear_timeout", _lib.mla_test_arm_linear_timeout(int(wait_limit_ns)))
 
 
 def mla_block_norm(u, ld_u: int, w_post, gate, ld_gate: int, alpha: float, residual, residual_out, w_pre, eps: float,

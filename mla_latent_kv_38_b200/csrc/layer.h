@@ -39,6 +39,8 @@ struct LinearShape {
     size_t smem;
 };
 LinearShape linear_i8_shape(int n_tok, int d_in, int d_out);
+// Test hook: the next product withholds one load and bounds its waits by wait_limit_ns.
+void linear_i8_arm_timeout_test(uint64_t wait_limit_ns);
 
 // pool: bf16 rows of d_c + d_r values, or (e4m3) rows in the layout of
 // mla_e4m3_row_bytes; q, q_c and q_r may be null together

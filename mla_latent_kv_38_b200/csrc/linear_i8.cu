@@ -28,7 +28,6 @@
 namespace mla {
 namespace {
 
-constexpr uint64_t kTimeoutNs = 2000000000ull;   // bound of every wait
 constexpr int kSms = 148;
 constexpr uint32_t kChunk = 128;                 // columns (bytes) of one K chunk
 constexpr uint32_t kOpBytes = 128 * kChunk;      // a chunk of 128 operand rows (16 KB)
@@ -43,13 +42,19 @@ bool make_map_i8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Every wait's bound, and the test hook's withheld load.
+struct WaitBound {
+    uint64_t timeout_ns;
+    int withhold;   // 1: the first CTA (or pair) never issues its first load of the activations
+};
+
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             int32_t* status) {
+                                             int32_t* status, const WaitBound& bound) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::global_timer_ns();
     while (!ptx::mbar_try_wait_suspend(bar, parity, 100000)) {
         if (*abort_flag) return false;
-        if (ptx::global_timer_ns() - t0 > kTimeoutNs) {
+        if (ptx::global_timer_ns() - t0 > bound.timeout_ns) {
             *abort_flag = 1;
             raise_status(status, MLA_STATUS_TIMEOUT);
             return false;
@@ -92,6 +97,7 @@ struct SplitArgs {
     int32_t* status;
     int n_tok, d_out, nt, chunks, stages;
     uint32_t idesc, tmem_cols, ring_bytes;
+    WaitBound bound;
 };
 
 __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __grid_constant__ SplitArgs p) {
@@ -151,13 +157,14 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
             const int s = c % S;
             bool ok = true;
             if (lane == (c & 7)) {
-                ok = wait_bounded(empty(s), ((c / S) & 1) ^ 1, abort_flag, p.status);
+                ok = wait_bounded(empty(s), ((c / S) & 1) ^ 1, abort_flag, p.status, p.bound);
                 if (ok) {
                     const uint32_t st = sbase + s * stage_bytes;
                     const int k = static_cast<int>(kChunk) * (c0 + c);
                     ptx::mbar_arrive_expect_tx(full(s), stage_bytes);
                     ptx::tma_load_2d(st, &p.tm_w, k, o0, full(s));
-                    ptx::tma_load_2d(st + kOpBytes, &p.tm_x, k, n0, full(s));
+                    const bool withheld = p.bound.withhold && c == 0 && (blockIdx.x | blockIdx.y) == 0;
+                    if (!withheld) ptx::tma_load_2d(st + kOpBytes, &p.tm_x, k, n0, full(s));
                 }
             }
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
         bool ok = true;
         for (int c = 0; c < c1 - c0 && ok; ++c) {
             const int s = c % S;
-            ok = __all_sync(0xffffffffu, wait_bounded(full(s), (c / S) & 1, abort_flag, p.status));
+            ok = __all_sync(0xffffffffu, wait_bounded(full(s), (c / S) & 1, abort_flag, p.status, p.bound));
             if (!ok) break;
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
         if (ptx::elect_one()) ptx::mma1_commit(done);
     }
     __syncwarp();
-    wait_bounded(done, 0, abort_flag, p.status);
+    wait_bounded(done, 0, abort_flag, p.status, p.bound);
     settle_copies(abort_flag);
     __syncthreads();   // every copy into the ring has landed and been read
     griddep_launch_dependents();
@@ -275,6 +282,7 @@ struct WideArgs {
     int whole;            // 256 x 256 tiles, in front of
     int pieces;           // pieces of 256 / cut channels of the others
     int cut;              // 1, 2 or 4
+    WaitBound bound;
 };
 
 // The tiles of a cluster: t = cluster, cluster + clusters, .. < whole + pieces.
@@ -347,11 +355,13 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                 const int s = e % kWideStages;
                 bool good = true;
                 if (lane == s) {
-                    good = wait_bounded(bar(W_EMPTY + s), ((e / kWideStages) & 1) ^ 1, abort_flag, p.status);
+                    good = wait_bounded(bar(W_EMPTY + s), ((e / kWideStages) & 1) ^ 1, abort_flag, p.status, p.bound);
                     if (good) {
                         const uint32_t st = sbase + s * kWideStage;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(bar(W_FULL + s), tx);
-                        ptx::tma_load_2d_pair_normal(st, &p.tm_x, static_cast<int>(kChunk) * c, n0, leader_bar(W_FULL + s));
+                        const bool withheld = p.bound.withhold && e == 0 && blockIdx.x == 0;
+                        if (!withheld)
+                            ptx::tma_load_2d_pair_normal(st, &p.tm_x, static_cast<int>(kChunk) * c, n0, leader_bar(W_FULL + s));
                         ptx::tma_load_2d_pair_normal(st + kOpBytes, tm_w, static_cast<int>(kChunk) * c, o0,
                                                      leader_bar(W_FULL + s));
                     }
@@ -366,12 +376,12 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             for (int t = cluster; t < p.whole + p.pieces && ok; t += clusters, ++i) {
                 const int b = i & 1;
                 const uint32_t idesc = ptx::idesc_i8_s32(256, wide_tile(p, t).cols);
-                ok = __all_sync(0xffffffffu, wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status));
+                ok = __all_sync(0xffffffffu, wait_bounded(bar(W_ACC_FREE + b), ((i >> 1) & 1) ^ 1, abort_flag, p.status, p.bound));
                 if (!ok) break;
                 ptx::tc_fence_after();
                 for (int c = 0; c < p.chunks; ++c, ++e) {
                     const int s = e % kWideStages;
-                    ok = __all_sync(0xffffffffu, wait_bounded(bar(W_FULL + s), (e / kWideStages) & 1, abort_flag, p.status));
+                    ok = __all_sync(0xffffffffu, wait_bounded(bar(W_FULL + s), (e / kWideStages) & 1, abort_flag, p.status, p.bound));
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
@@ -393,7 +403,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                 if (ptx::elect_one()) ptx::mma_commit_pair(bar(W_DRAIN), 0x1);
                 __syncwarp();
                 const uint64_t t0 = ptx::global_timer_ns();
-                while (!ptx::mbar_try_wait(bar(W_DRAIN), 0) && ptx::global_timer_ns() - t0 < kTimeoutNs) {
+                while (!ptx::mbar_try_wait(bar(W_DRAIN), 0) && ptx::global_timer_ns() - t0 < p.bound.timeout_ns) {
                 }
             }
         }
@@ -419,7 +429,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
             scales[st] = o0 + st < p.d_out ? p.w_scale[o0 + st] : 0.f;
             const float sx = row0 + lane < p.n_tok ? p.x_scale[row0 + lane] : 0.f;
             ptx::named_bar_sync(2, 256);
-            bool ok = wait_bounded(bar(W_ACC_FULL + b), (i >> 1) & 1, abort_flag, p.status);
+            bool ok = wait_bounded(bar(W_ACC_FULL + b), (i >> 1) & 1, abort_flag, p.status, p.bound);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
 #pragma unroll 1
@@ -518,6 +528,14 @@ long wide_cost(int n_tok, int chunks, int d_out) {
     return 6000 + (tiles + kSms / 2 - 1) / (kSms / 2) * (chunks * 620L + 500);
 }
 
+// Test hook state: the next launch withholds one load and uses this wait bound.
+std::atomic<uint64_t> g_test_wait_limit_ns{0};
+
+WaitBound next_bound() {
+    const uint64_t limit = g_test_wait_limit_ns.exchange(0);
+    return limit != 0 ? WaitBound{limit, 1} : WaitBound{2000000000ull, 0};
+}
+
 int chunks_of(int d_in) { return (d_in + static_cast<int>(kChunk) - 1) / static_cast<int>(kChunk); }
 
 // Launch shape of the split kernel.  Its dynamic shared memory is at least its
@@ -561,7 +579,7 @@ cudaError_t launch_split(const int8_t* x8, long ld_x, const float* x_scale, cons
     p.nt = shape.nt, p.stages = shape.stages, p.ring_bytes = shape.ring_bytes, p.tmem_cols = shape.tmem_cols;
     p.idesc = ptx::idesc_i8_s32(128, p.nt);
     p.x_scale = x_scale, p.w_scale = w_scale, p.out = out, p.status = status;
-    p.n_tok = n_tok, p.d_out = d_out;
+    p.n_tok = n_tok, p.d_out = d_out, p.bound = next_bound();
     if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) || !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, p.nt))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> smem_set{0};
@@ -582,7 +600,7 @@ cudaError_t launch_wide(const int8_t* x8, long ld_x, const float* x_scale, const
     p.whole = p.cut > 1 ? tiles - rest : tiles;
     p.pieces = p.cut > 1 ? rest * p.cut : 0;
     p.x_scale = x_scale, p.w_scale = w_scale, p.status = status;
-    p.n_tok = n_tok, p.d_out = d_out;
+    p.n_tok = n_tok, p.d_out = d_out, p.bound = next_bound();
     if (!make_map_i8(&p.tm_w, w8, d_in, d_out, d_in, 128) ||
         !make_map_i8(&p.tm_w_cut, w8, d_in, d_out, d_in, 128 / p.cut) ||
         !make_map_i8(&p.tm_x, x8, d_in, n_tok, ld_x, 128) ||
@@ -615,6 +633,8 @@ cudaError_t launch_linear_i8(const int8_t* x8, long ld_x, const float* x_scale, 
         return launch_wide(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, status, stream);
     return launch_split(x8, ld_x, x_scale, w8, w_scale, out, n_tok, d_in, d_out, plan, status, stream);
 }
+
+void linear_i8_arm_timeout_test(uint64_t wait_limit_ns) { g_test_wait_limit_ns.store(wait_limit_ns); }
 
 LinearShape linear_i8_shape(int n_tok, int d_in, int d_out) {
     SplitPlan plan;

@@ -599,6 +599,12 @@ int mla_linear_i8_shape(int n_tok, int d_in, int d_out, int* cluster, int* tmem_
     return MLA_OK;
 }
 
+int mla_test_arm_linear_timeout(uint64_t wait_limit_ns) {
+    if (wait_limit_ns == 0 || wait_limit_ns > 2000000000ull) return MLA_ERR_SIZE;
+    mla::linear_i8_arm_timeout_test(wait_limit_ns);
+    return MLA_OK;
+}
+
 int mla_block_norm(const mla_bf16* u, int64_t ld_u, const mla_bf16* w_post, const mla_bf16* gate,
                    int64_t ld_gate, float alpha, const mla_bf16* residual, mla_bf16* residual_out,
                    const mla_bf16* w_pre, float eps, int n_tok, int d, mla_bf16* out, int8_t* out8,
