@@ -1395,15 +1395,18 @@ mla_sm100_schedule_kernel(const int32_t* __restrict__ seq_lens, const UnitMap um
 // from L2 (ld.global.cg).  The first slots' rows are fetched together with the
 // log-sum-exps, so that a row split in two takes two dependent round trips
 // (metadata, then everything else); further slots follow kSlots at a time.
-// Blocks of 8 warps, at most 64 registers a thread: 4 blocks per SM, one wave
-// for the 4,096 rows of 32 split units.  (Blocks of 4 warps doubled the merge
+// Blocks of 8 warps; mla_decode's form at most 64 registers a thread: 4 blocks
+// per SM, one wave for the 4,096 rows of 32 split units; the shared decode's
+// forms up to 80: 3 blocks.  (Blocks of 4 warps doubled the merge
 // at prefill sizes, where most of the U x 128 rows belong to whole units and
 // the time goes into scheduling blocks that exit at once; one wave of blocks
 // that walk the rows was no faster.)
 //
 // kWarps warps per row, 512 / kWarps columns each, with 2 kWarps partials on
 // their way at a time: one for many rows, four for the few rows of a small
-// shared decode, which may have dozens of partials each.
+// shared decode, which may have dozens of partials each: 16 rows behind 64,000
+// shared keys 51.0 us with one warp a row, 43.8 with four (whole call); 464
+// rows behind 1,024 keys 23.3 and 23.0.
 template <bool kShared, int kWarps>
 __global__ void __launch_bounds__(256, kShared ? 3 : 4)
 mla_sm100_merge_kernel(const int4* __restrict__ unit_meta, const float* __restrict__ part_o,
@@ -1672,7 +1675,9 @@ cudaError_t launch_units(const DecodeParams& P, const UnitMap& um, int U, size_t
     e = launch_pdl(mla_decode_sm100_kernel<kShared>, dim3(2 * kClusters), dim3(kThreads), kSmemBytes, stream, k);
     if (e != cudaSuccess) return e;
     const int rows = kShared ? um.n_rows : U * 128;
-    const bool few = kShared && rows <= 148 * 8;   // four warps a row still make one wave
+    // four warps a row, two rows a block, while that makes one wave of three
+    // blocks an SM (1,024 rows 28.8 us with four warps a row, 26.4 with one)
+    const bool few = kShared && rows <= 2 * kClusters * 3 * 2;
     return launch_pdl(few ? mla_sm100_merge_kernel<kShared, kShared ? 4 : 1> : mla_sm100_merge_kernel<kShared, 1>,
                       dim3(few ? (rows + 1) / 2 : (rows + 7) / 8), dim3(256), 0, stream,
                       static_cast<const int4*>(k.unit_meta), static_cast<const float*>(k.part_o),

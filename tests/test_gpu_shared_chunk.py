@@ -53,3 +53,25 @@ def test_a_chunk_matches_mla_decode(M, n_h, T_q):  # noqa: F811
     # each side rounds its weights and its result to bf16
     assert ((lat[:n].float() - c.latent[:n].float()).abs() <= 4 * BF * lat[:n].float().abs().clamp(min=0.25)).all()
     assert ((lse[:n] - c.lse[:n]).abs() <= 2 * SCORE).all()
+
+
+@pytest.mark.parametrize("n_h,B", [(8, 111), (8, 112), (7, 127), (16, 74), (127, 7)])
+def test_row_counts_around_the_merges_two_forms(M, n_h, B):  # noqa: F811
+    c = Case(M, n_h, *V2, 1, 6, [1 + (37 * b) % 130 for b in range(B)], 0)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("impl", [0, 1])
+@pytest.mark.parametrize("n_h,B", [(16, 12), (128, 2)])
+def test_a_table_without_room_behind_the_shared_pages(M, n_h, B, impl):  # noqa: F811
+    """n_shared = max_blocks_per_seq: no sequence has a valid length, with and without units of the shared pages."""
+    c = Case(M, n_h, *V2, 1, 8, [0] * B, impl, spare=-1)
+    assert c.mb == 8
+    c.lens.fill_(64 * 8)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == M.MLA_STATUS_BAD_SEQ_LEN
+    c.check()
