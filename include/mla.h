@@ -163,7 +163,8 @@ int mla_absorb_q(const mla_config_t* cfg, const mla_bf16* q_c, const mla_bf16* w
  *   positions  (n_tok) int32
  *   rope_table (max_pos, d_r) float32 from mla_rope_table
  *   block_table (B, max_blocks_per_seq) int32
- *   pool       (num_blocks, block_size, d_c + d_r) bf16
+ *   pool       (num_blocks, block_size, d_c + d_r) bf16; the tokens of a call
+ *              go to different rows of it (two on one row mix there)
  *   dev_status one int32 on the device (may be NULL): MLA_STATUS_* bits are
  *              OR-ed in for rows whose position or block index is invalid;
  *              those rows are not written. */
@@ -203,6 +204,10 @@ size_t mla_decode_workspace_bytes(const mla_config_t* cfg, int B, int T_q, int m
  * Partial results (fp32 latent rows and log-sum-exp) of split rows go to the
  * workspace and are merged by a log-sum-exp reduction kernel.  The workspace
  * starts with the device status word (mla_read_status).
+ * The tcgen05 kernels round each softmax weight to bf16 for the tensor cores
+ * (the latent is off by at most 2^-8 sum_j p_j |row_j| for it, besides its own
+ * rounding) and sum the weights, for the division and the lse, in float32
+ * before that; the portable kernels keep float32 weights.
  * A key whose score is NaN or +inf makes the latent and the lse of the rows
  * that see it NaN.
  * Sizes: B * T_q <= 65535 query rows (and B * T_q * n_h / 128 <= 65535 units
@@ -380,9 +385,10 @@ int mla_decode_e4m3(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf
  * behind one prompt, the output projection and the residual add. */
 
 /* mla_decode for a batch whose sequences begin with the same cache pages (a
- * system prompt, few-shot examples): the same scores, mask, softmax, outputs
- * and size limits, with the keys of the shared pages read once for all query
- * rows of the batch instead of once per sequence.
+ * system prompt, few-shot examples): the same scores, mask, softmax, roundings,
+ * outputs and size limits.  The shared pages lie in the pool once, and a walk
+ * over them serves up to 128 query rows, whatever their sequence, where
+ * mla_decode walks them for each sequence and block of 128 heads.
  *   shared_table (n_shared) int32: the blocks of the shared pages, which hold
  *     the first 64 * n_shared keys of every sequence.  Only whole pages are
  *     shared.  n_shared = 0 shares nothing (shared_table may be NULL).
@@ -395,14 +401,16 @@ int mla_decode_e4m3(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf
  *     sequence that breaks this sets MLA_STATUS_BAD_SEQ_LEN; its outputs are
  *     zero and -inf.
  * A key that only a step's later tokens see does not reach the tokens before
- * them, whatever it holds.
+ * them, whatever it holds.  A row that sees a score of NaN or +inf is NaN, its
+ * lse too.  A score of -inf is a weight of zero: where an infinity in the key's
+ * latent made it, the row is NaN in that column (0 inf).
  * tcgen05 kernels (cfg->impl 0 or 2): d_c = 512, d_r = 64 and any n_h, with
  * B * T_q * ceil(n_h / 128) * max_blocks_per_seq < 2^29 (MLA_ERR_SIZE beyond).
  * They work on units of up to 128 query rows.  A unit of whole tokens of one
- * sequence walks the shared pages and its own; where such units would leave too
- * many of the 128 rows empty, the shared pages are walked by units of 128
- * consecutive rows of the batch, whatever their sequence, and the results of
- * the two key ranges joined by their log-sum-exps.  Portable kernels: every
+ * sequence walks the shared pages and its own (with 128 heads: each token);
+ * where such units would leave too many of the 128 rows empty, the shared pages
+ * are walked by units of 128 consecutive rows of the batch instead, and the
+ * results of the two key ranges joined by their log-sum-exps.  Portable kernels: every
  * supported shape, the two ranges always apart.  max_splits as for mla_decode,
  * for each walk. */
 int mla_decode_shared(const mla_config_t* cfg, const mla_bf16* q_abs, const mla_bf16* q_r,
@@ -494,7 +502,7 @@ int mla_block_norm(const mla_bf16* u, int64_t ld_u, const mla_bf16* w_post, cons
  *   kv (n_tok, d_c + d_r) bf16, rows ld_kv elements apart (ld_kv >= d_c + d_r,
  *      a multiple of 8): W^DKV's rows, or the last columns of a wider product
  *   w_kv (d_c) bf16;  eps > 0;  rope_table 16-byte aligned;
- *      the rest as for mla_rope_append
+ *      the rest as for mla_rope_append.  The sum of c^2 stays in float32's range
  *   q_c (n_tok, n_h, d_h), q_r (n_tok, n_h, d_r) bf16, dense, apart from q
  * A token whose position is invalid sets MLA_STATUS_BAD_POSITION and leaves
  * q_c, q_r and the cache as they were; one whose block is invalid sets

@@ -42,7 +42,7 @@ bool make_map_i8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Every wait's bound, and the test hook's withheld load.
+// The bound of every mbarrier wait, and the test hook's withheld load.
 struct WaitBound {
     uint64_t timeout_ns;
     int withhold;   // 1: the first CTA (or pair) never issues its first load of the activations
@@ -85,8 +85,9 @@ constexpr size_t tmem_share(uint32_t cols) { return kSmSmem / 512 * cols - 1024;
 
 constexpr int kSplitThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kSplitRing = 200 * 1024;       // one CTA per SM
-constexpr uint32_t kSplitRingHalf = 108 * 1024;   // two
+// A CTA's ring at most (shorter where K is): with one CTA per SM, with two
+constexpr uint32_t kSplitRing = 200 * 1024;
+constexpr uint32_t kSplitRingHalf = 108 * 1024;
 
 struct SplitArgs {
     CUtensorMap tm_w;   // w8 [d_out][d_in], boxes 128 x 128
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_i8_split_kernel(const __
                     const int k = static_cast<int>(kChunk) * (c0 + c);
                     ptx::mbar_arrive_expect_tx(full(s), stage_bytes);
                     ptx::tma_load_2d(st, &p.tm_w, k, o0, full(s));
-                    const bool withheld = p.bound.withhold && c == 0 && (blockIdx.x | blockIdx.y) == 0;
+                    const bool withheld = c == 0 && (blockIdx.x | blockIdx.y) == 0 && p.bound.withhold;
                     if (!withheld) ptx::tma_load_2d(st + kOpBytes, &p.tm_x, k, n0, full(s));
                 }
             }
@@ -359,7 +360,7 @@ linear_i8_wide_kernel(const __grid_constant__ WideArgs p) {
                     if (good) {
                         const uint32_t st = sbase + s * kWideStage;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(bar(W_FULL + s), tx);
-                        const bool withheld = p.bound.withhold && e == 0 && blockIdx.x == 0;
+                        const bool withheld = e == 0 && blockIdx.x == 0 && p.bound.withhold;
                         if (!withheld)
                             ptx::tma_load_2d_pair_normal(st, &p.tm_x, static_cast<int>(kChunk) * c, n0, leader_bar(W_FULL + s));
                         ptx::tma_load_2d_pair_normal(st + kOpBytes, tm_w, static_cast<int>(kChunk) * c, o0,

@@ -1060,6 +1060,8 @@ mla_decode_sm100_kernel(const __grid_constant__ Sm100Params p) {
             m_used = new_m;
 
             // The weights of row m, keys key0 + [0, 64) (a masked score's is 2^-inf = 0).
+            // The tensor cores take them as bf16 beside the bf16 values (off by 2^-8 of
+            // each at most); their sum keeps them in float32, and with it the lse.
             float ps2[2] = {0.f, 0.f};
             const float neg_m = kShared && m_used == -INFINITY ? 0.f : -m_used;
             uint32_t pk[32];
