@@ -311,11 +311,12 @@ decode_simt_kernel(DecodeParams P) {
 }
 
 // Split-KV merge: o = sum_s w_s o_s / sum_s w_s, lse = max + log sum_s w_s with
-// w_s = exp(lse_s - max).  One block per (token, head).
+// w_s = exp(lse_s - max).  One block per (token, head).  skip_empty: a part with
+// an lse of -inf is all zeros (elsewhere it may hold the NaN of a key at -inf).
 __global__ void __launch_bounds__(128)
 merge_splits_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                     uint16_t* __restrict__ out_latent, float* __restrict__ out_lse,
-                    int rows, int d_c, int splits) {
+                    int rows, int d_c, int splits, bool skip_empty) {
     const int row = blockIdx.x;
     float m = -INFINITY;
     for (int s = 0; s < splits; ++s) m = fmaxf(m, part_lse[static_cast<size_t>(s) * rows + row]);
@@ -329,6 +330,7 @@ merge_splits_kernel(const float* __restrict__ part_o, const float* __restrict__ 
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         for (int s = 0; s < splits; ++s) {
             const float ls = part_lse[static_cast<size_t>(s) * rows + row];
+            if (skip_empty && ls == -INFINITY) continue;
             const float w = ls == -INFINITY ? 0.f : ex2((ls - m) * kLog2e) * inv_z;
             const float4 v = *reinterpret_cast<const float4*>(
                 part_o + (static_cast<size_t>(s) * rows + row) * d_c + c);
@@ -359,7 +361,7 @@ cudaError_t launch_decode_simt(const DecodeParams& P, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess || P.splits == 1) return e;
     return launch_merge(P.part_o, P.part_lse, P.out_latent, P.out_lse, P.n_tok * P.n_h, P.d_c,
-                        P.splits, stream);
+                        P.splits, true, stream);
 }
 
 cudaError_t launch_decode_shared_simt(const DecodeParams& P, cudaStream_t stream) {
@@ -373,13 +375,13 @@ cudaError_t launch_decode_shared_simt(const DecodeParams& P, cudaStream_t stream
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_merge(P.part_o, P.part_lse, P.out_latent, P.out_lse, static_cast<int>(rows), P.d_c, 2 * P.splits,
-                        stream);
+                        false, stream);
 }
 
 cudaError_t launch_merge(const float* part_o, const float* part_lse, uint16_t* out_latent,
-                         float* out_lse, int rows, int d_c, int splits, cudaStream_t stream) {
+                         float* out_lse, int rows, int d_c, int splits, bool skip_empty, cudaStream_t stream) {
     merge_splits_kernel<<<rows, 128, 0, stream>>>(part_o, part_lse, out_latent, out_lse, rows, d_c,
-                                                  splits);
+                                                  splits, skip_empty);
     return cudaGetLastError();
 }
 

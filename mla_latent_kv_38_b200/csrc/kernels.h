@@ -29,7 +29,7 @@ size_t simt_smem_bytes(int d_c, int d_r, bool e4m3);
 cudaError_t launch_decode_simt(const DecodeParams& P, cudaStream_t stream);
 cudaError_t launch_decode_shared_simt(const DecodeParams& P, cudaStream_t stream);
 cudaError_t launch_merge(const float* part_o, const float* part_lse, uint16_t* out_latent,
-                         float* out_lse, int rows, int d_c, int splits, cudaStream_t stream);
+                         float* out_lse, int rows, int d_c, int splits, bool skip_empty, cudaStream_t stream);
 
 cudaError_t launch_absorb_q_simt(const uint16_t* q_c, const uint16_t* w_uk, uint16_t* q_abs,
                                  int n_tok, int n_h, int d_h, int d_c, cudaStream_t stream);
